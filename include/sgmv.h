@@ -1,6 +1,10 @@
 /*
  * sgmv.h — C ABI of the MI355X (gfx950) SGMV library.
  *
+ * SGMV itself comes first; the paged key/value cache that a serving layer
+ * needs next to it (block tables, rotary write, attention) has its own part
+ * below.
+ *
  * SGMV (segmented gather matrix-vector multiplication) applies many LoRA
  * adapters to one batch in one pass. The batch's rows are grouped into
  * contiguous segments; segment s covers rows seg_start[s] .. seg_start[s+1]-1
@@ -92,7 +96,7 @@ enum sgmv_status {
     SGMV_ERR_SHAPE = -2,     /* negative size, d not a multiple of 8, or too large */
     SGMV_ERR_RANK = -3,      /* r not in {8, 16, 32, 64} */
     SGMV_ERR_DTYPE = -4,     /* dtype not SGMV_F32 / SGMV_BF16 */
-    SGMV_ERR_ALIGN = -5,     /* X, Y or V not 16-byte aligned */
+    SGMV_ERR_ALIGN = -5,     /* an operand (or a row of it) not 16-byte aligned */
     SGMV_ERR_WORKSPACE = -6, /* workspace missing or smaller than sgmv_workspace_bytes */
     SGMV_ERR_HIP = -7,       /* the HIP runtime reported an error at launch */
     SGMV_ERR_ADAPTER = -8,   /* host metadata: an adapter id that is negative (or outside the pool) */
@@ -379,6 +383,150 @@ int sgmv_workspace_status(const void *workspace, uint32_t *status, void *stream)
  * path from the host.
  */
 uint32_t sgmv_set_wait_limit(uint32_t polls);
+
+/* ---------------------------------------------------------------------------
+ * The paged key/value cache between a layer's q/k/v and o projections
+ * ---------------------------------------------------------------------------
+ * What runs between the projections SGMV adapts: the step's tokens get cache
+ * slots (sgmv_kv_tables, once per step), q and k are rotated and k and v
+ * written to the cache (sgmv_rope_append, per layer), and the step's queries
+ * attend to the cache (sgmv_paged_attention, per layer).
+ *
+ * K_cache, V_cache  device, [num_pages][kv_heads][page_size][head_dim],
+ *               contiguous, 16-byte aligned: one head of one page is one run
+ *               of memory.
+ * page_size     16, 32, 64, 128 or 256; num_pages * page_size < 2^31.
+ * head_dim      a positive multiple of 8, at most 128.
+ * block_table   device int32[num_requests][max_blocks]: entry [b][i] is the
+ *               page of positions i * page_size ... of request b.
+ * q_start       device int32[num_requests + 1], non-decreasing from 0: request
+ *               b's new tokens are rows q_start[b] .. q_start[b+1]-1 of the
+ *               step's T rows.
+ * kv_len        device int32[num_requests]: tokens of request b in the cache,
+ *               its new ones included. New token i of n is at position
+ *               kv_len[b] - n + i.
+ * slot          device int32[T]: page * page_size + offset in the page, or a
+ *               negative value for a token that has none.
+ * q, k, v       rows of heads, [T][heads][head_dim] with a row stride in
+ *               elements (rows may be slices of one fused projection's
+ *               output); rows start 16-byte aligned.
+ * Streams, ownership and errors are as above: nothing is allocated, nothing
+ * synchronises, and no device-resident value makes a kernel read or write
+ * outside the documented buffers. Page ids outside [0, num_pages) are never
+ * followed (what such an entry's positions hold is then unspecified). */
+
+/*
+ * Block tables and slots of one step, built on the device from the requests'
+ * lengths. For request b with seq_len[b] cached tokens:
+ *   new_len[b] >= 0  adds that many tokens. Pages it needs beyond the ones it
+ *                    has are taken from the ring of free pages, requests in
+ *                    order, and entered in its row of block_table.
+ *   new_len[b] < 0   the request has ended: its pages go back to the ring (for
+ *                    later calls), and its length becomes 0.
+ * A request whose pages do not fit what is free, or its row of block_table,
+ * is refused: it gets no page and no slot and keeps its length. Requests are
+ * served in order until one does not fit; after it only those that need no
+ * page are. (One too long for its row of block_table takes no part in this.)
+ *
+ * free_pages   device int32[num_pages], a ring of the free pages' ids.
+ * pool_in      device int32[4]: [0] the ring's first free entry (in
+ *              [0, num_pages)), [1] the number of free pages.
+ * pool_out     device int32[4]: the same after the call, [2] the number of
+ *              requests refused, [3] the step's tokens (q_start's last).
+ * q_start      out; kv_len out: the lengths after the step.
+ * position     out, int32[T]: each token's position, -1 past the last token.
+ * slot         out, int32[T]: each token's slot, -1 where it has none.
+ * The outputs must not overlap the inputs (the next call's seq_len and
+ * pool_in are this one's kv_len and pool_out: keep two of each). Calling
+ * twice with the same inputs and the same free_pages and block_table gives
+ * the same result. num_requests: at most SGMV_MAX_REQUESTS.
+ */
+#define SGMV_MAX_REQUESTS 8192
+
+int sgmv_kv_tables(const int32_t *seq_len, const int32_t *new_len, int32_t num_requests, int32_t *block_table,
+                   int32_t max_blocks, int32_t page_size, int32_t *free_pages, int32_t num_pages,
+                   const int32_t *pool_in, int32_t *pool_out, int32_t *q_start, int32_t *kv_len,
+                   int32_t *position, int32_t *slot, int32_t T, void *stream);
+
+/*
+ * Rotary table: table[p][i] = (cos, sin) of position p's angle for pair i,
+ * float[max_position][rot_dim / 2][2], formed in 64 bits and rounded once.
+ * With inverse frequencies f_i = base^(-2i / rot_dim), the angle is
+ *   SGMV_ROPE_PLAIN     p * f_i
+ *   SGMV_ROPE_LINEAR    p * f_i / factor (positions interpolated)
+ *   SGMV_ROPE_BY_PARTS  p * (f_i * w_i + f_i / factor * (1 - w_i)) (YaRN, Peng
+ *                       et al. 2023): w_i falls linearly from 1 to 0 in i
+ *                       between the pairs that turn beta_fast and beta_slow
+ *                       times over original_max positions, and cos and sin are
+ *                       multiplied by 0.1 ln(factor) + 1.
+ * For SGMV_ROPE_PLAIN the scaling fields are not read.
+ */
+enum sgmv_rope_kind { SGMV_ROPE_PLAIN = 0, SGMV_ROPE_LINEAR = 1, SGMV_ROPE_BY_PARTS = 2 };
+
+int sgmv_rope_table(float *table, int32_t max_position, int32_t rot_dim, double base, int32_t kind,
+                    double factor, double beta_fast, double beta_slow, int32_t original_max, void *stream);
+
+/*
+ * Rotates the first rot_dim elements of every head of q and k by their
+ * token's position and writes k and v to the cache:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * with pairs (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) when interleaved.
+ * Elements past rot_dim, and v, are copied. Arithmetic is fp32, rounded once.
+ *
+ * q_out        out, [T][q_heads][head_dim] with its own row stride; may be q.
+ * table        of sgmv_rope_table; not read (may be NULL) when rot_dim is 0.
+ * rot_dim      a multiple of 16, 0 .. head_dim.
+ * position     device int32[T]; a token whose position is outside
+ *              [0, max_position) is left out (nothing of it is written).
+ * slot         device int32[T]; a token without a slot (or one outside the
+ *              cache) has its q rotated, and no k and v written.
+ * q, q_out     may be NULL with q_heads = 0; k and v may be NULL with
+ *              kv_heads = 0 (then the cache and slot may be too).
+ * Two tokens must not have one slot.
+ */
+int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, int32_t q_heads,
+                     const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *K_cache,
+                     void *V_cache, int32_t num_pages, int32_t kv_heads, int32_t page_size, int32_t head_dim,
+                     const int32_t *position, const int32_t *slot, int32_t T, const float *table,
+                     int32_t max_position, int32_t rot_dim, int32_t interleaved, int32_t dtype, void *stream);
+
+/*
+ * Attention of the step's new tokens over the paged cache (which holds them
+ * already). Query head h of a token at position p reads cached head
+ * h / (q_heads / kv_heads) and sees key j of its request when
+ *     0 <= j <= p,  and with window > 0 also  j > p - window  or  j < sinks:
+ * a sliding window, with the first `sinks` tokens always visible.
+ *     out = sum_j w_j V_j / sum_j w_j,   w_j = exp(scale * q . K_j)
+ *     lse = log(sum_j w_j)
+ * A row that sees no key gets out = 0 and lse = -infinity. Keys that no row
+ * of a request sees are not used, whatever they hold. Rows of no request are
+ * left as they were.
+ *
+ * Products accumulate in fp32 and the softmax's running maximum, sum and
+ * output are fp32; with bf16 the weights enter the second product rounded to
+ * bf16, and out is rounded once. Results do not depend on timing.
+ *
+ * out          [T][q_heads][head_dim] with its own row stride.
+ * lse          device float[T][q_heads], or NULL.
+ * q_heads      a multiple of kv_heads.
+ * max_q_len    at least the largest number of new tokens of a request (the
+ *              first max_q_len of more are computed).
+ * scale        positive and finite. window, sinks: >= 0.
+ * workspace    as sgmv_paged_attention_workspace_bytes says for the same
+ *              sizes, 256-byte aligned, zero-filled before its first use; its
+ *              counters are zero again after every call. Not to be shared
+ *              with the calls above or between calls that overlap in time.
+ */
+int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t q_stride,
+                         int32_t q_heads, const void *K_cache, const void *V_cache, int32_t num_pages,
+                         int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *block_table,
+                         int32_t max_blocks, const int32_t *q_start, const int32_t *kv_len,
+                         int32_t num_requests, int32_t T, int32_t max_q_len, float scale, int32_t window,
+                         int32_t sinks, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of sgmv_paged_attention (0 on invalid arguments); the same
+ * for every batch of the layout. */
+size_t sgmv_paged_attention_workspace_bytes(int32_t head_dim, int32_t dtype);
 
 /* A static, human-readable name for a status code. */
 const char *sgmv_status_string(int status);

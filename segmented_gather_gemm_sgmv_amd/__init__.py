@@ -29,7 +29,8 @@ SGMV_OK = 0
 _DTYPES = {torch.float32: SGMV_F32, torch.bfloat16: SGMV_BF16}
 
 # (name, restype, argtypes) for every symbol include/sgmv.h declares.
-_i32, _i64, _vp, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
+_i32, _i64, _vp, _f32, _f64, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double,
+                                    ctypes.c_size_t)
 EXPORTS = {
     "sgmv_shrink": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
                                    _sz, _vp]),
@@ -55,6 +56,15 @@ EXPORTS = {
     "sgmv_stream_probe": (ctypes.c_int, [_vp, _sz, _vp, _i32, _vp]),
     "sgmv_workspace_status": (ctypes.c_int, [_vp, _vp, _vp]),
     "sgmv_set_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),
+    "sgmv_kv_tables": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _i32, _vp]),
+    "sgmv_rope_table": (ctypes.c_int, [_vp, _i32, _i32, _f64, _i32, _f64, _f64, _f64, _i32, _vp]),
+    "sgmv_rope_append": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _i32,
+                                        _i32, _i32, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "sgmv_paged_attention": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                            _i32, _vp, _vp, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp, _sz,
+                                            _vp]),
+    "sgmv_paged_attention_workspace_bytes": (_sz, [_i32, _i32]),
     "sgmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sgmv_version": (ctypes.c_int, []),
 }
@@ -484,6 +494,174 @@ def sgmv_stream_probe(src: torch.Tensor, sink: torch.Tensor, nbytes: Optional[in
     _check("sgmv_stream_probe", st)
 
 
+# -- the paged key/value cache ---------------------------------------------------
+SGMV_MAX_REQUESTS = 8192
+SGMV_ROPE_PLAIN, SGMV_ROPE_LINEAR, SGMV_ROPE_BY_PARTS = 0, 1, 2
+
+
+def _rows3(t: torch.Tensor, name: str, dtype, head_dim: Optional[int] = None) -> Tuple[int, int]:
+    """(address, row stride in elements) of rows of heads [T, heads, head_dim]:
+    heads packed within a row, rows any distance apart."""
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have 3 dimensions")
+    if head_dim is not None and shape[2] != head_dim:
+        raise ValueError(f"{name} must have heads of {head_dim}")
+    if (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a row must be packed")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _ints(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on a GPU device")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _cache(K: torch.Tensor, V: torch.Tensor, dtype) -> Tuple[int, int, int, int, int]:
+    """(pages, kv_heads, page_size, head_dim) of a K/V cache pair."""
+    if K.dtype is not dtype or V.dtype is not dtype:
+        raise TypeError(f"K_cache and V_cache must be {dtype}")
+    if K.dim() != 4 or K.shape != V.shape or not K.is_contiguous() or not V.is_contiguous() or not K.is_cuda:
+        raise ValueError("K_cache and V_cache must be contiguous [pages, kv_heads, page_size, head_dim] GPU tensors "
+                         "of one shape")
+    return K.shape
+
+
+def sgmv_kv_tables(seq_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, page_size: int,
+                   free_pages: torch.Tensor, pool_in: torch.Tensor, pool_out: torch.Tensor, q_start: torch.Tensor,
+                   kv_len: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, stream=None) -> None:
+    """One step's block tables and slots from the requests' lengths: requests
+    that add new_len >= 0 tokens get pages from the ring of free pages, ended
+    ones (new_len < 0) give theirs back; q_start, kv_len, position, slot and
+    pool_out are written (see include/sgmv.h). Nothing is read on the host."""
+    B = seq_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per request")
+    T = slot.numel()
+    st = lib.sgmv_kv_tables(_ints(seq_len, "seq_len"), _ints(new_len, "new_len", B), B,
+                            _ints(block_table, "block_table"), block_table.shape[1], page_size,
+                            _ints(free_pages, "free_pages"), free_pages.numel(), _ints(pool_in, "pool_in", 4),
+                            _ints(pool_out, "pool_out", 4), _ints(q_start, "q_start", B + 1),
+                            _ints(kv_len, "kv_len", B), _ints(position, "position", T), _ints(slot, "slot"), T,
+                            _stream(seq_len, stream))
+    _check("sgmv_kv_tables", st)
+
+
+def sgmv_rope_table(max_position: int, rot_dim: int, base: float = 10000.0, kind: int = SGMV_ROPE_PLAIN,
+                    factor: float = 1.0, beta_fast: float = 32.0, beta_slow: float = 1.0, original_max: int = 0,
+                    device="cuda", stream=None) -> torch.Tensor:
+    """The rotary table [max_position, rot_dim / 2, 2] (cos, sin) that
+    sgmv_rope_append takes; see include/sgmv.h for the scalings. Kept for as
+    long as the model is served."""
+    table = torch.empty((max_position, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    st = lib.sgmv_rope_table(_dev(table, "table"), max_position, rot_dim, base, kind, factor, beta_fast, beta_slow,
+                             original_max, _stream(table, stream))
+    _check("sgmv_rope_table", st)
+    return table
+
+
+def sgmv_rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                     v: Optional[torch.Tensor], K_cache: Optional[torch.Tensor], V_cache: Optional[torch.Tensor],
+                     position: torch.Tensor, slot: Optional[torch.Tensor], table: Optional[torch.Tensor],
+                     interleaved: bool = False, stream=None) -> None:
+    """q_out = q rotated by each token's position; k, rotated, and v written to
+    the paged cache at each token's slot. Rows [T, heads, head_dim] with any
+    row stride; q_out may be q; q (with q_out) or k, v and the cache may be
+    None. table: of sgmv_rope_table (its rot_dim elements of a head turn), or
+    None to copy only."""
+    T = position.numel()
+    like = q if q is not None else k
+    if like is None:
+        raise ValueError("sgmv_rope_append needs q or k")
+    if like.dim() != 3 or like.shape[0] != T:
+        raise ValueError("q and k must have one row per token")
+    dtype, D = like.dtype, like.shape[2]
+    q_p = qo_p = k_p = v_p = K_p = V_p = slot_p = table_p = None
+    q_s = qo_s = k_s = v_s = q_heads = kv_heads = pages = rot_dim = 0
+    page, max_position = 16, 2 ** 31 - 1
+    if q is not None:
+        q_p, q_s = _rows3(q, "q", dtype)
+        qo_p, qo_s = _rows3(q_out, "q_out", dtype, D)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        q_heads = q.shape[1]
+    if k is not None:
+        k_p, k_s = _rows3(k, "k", dtype, D)
+        v_p, v_s = _rows3(v, "v", dtype, D)
+        pages, kv_heads, page, width = _cache(K_cache, V_cache, dtype)
+        if k.shape != v.shape or k.shape[0] != T or k.shape[1] != kv_heads or width != D:
+            raise ValueError("k and v must be [T, kv_heads, head_dim] as the cache has them")
+        K_p, V_p, slot_p = K_cache.data_ptr(), V_cache.data_ptr(), _ints(slot, "slot", T)
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("table must be [max_position, rot_dim / 2, 2]")
+        table_p, max_position, rot_dim = _dev(table, "table", torch.float32), table.shape[0], 2 * table.shape[1]
+    st = lib.sgmv_rope_append(qo_p, qo_s, q_p, q_s, q_heads, k_p, k_s, v_p, v_s, K_p, V_p, pages, kv_heads, page, D,
+                              _ints(position, "position"), slot_p, T, table_p, max_position, rot_dim,
+                              int(interleaved), _dtype_code(like), _stream(like, stream))
+    _check("sgmv_rope_append", st)
+
+
+_attention_workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
+
+
+def attention_workspace(device: torch.device, head_dim: int, dtype: torch.dtype, stream=None) -> torch.Tensor:
+    """A zero-filled workspace for sgmv_paged_attention, cached per (device,
+    stream). Its size depends on the head width and dtype alone; it is not the
+    SGMV calls' workspace."""
+    device = torch.device(device)
+    s = _torch_stream(device, stream)
+    key = (device.index, s.cuda_stream)
+    nbytes = int(lib.sgmv_paged_attention_workspace_bytes(head_dim, _DTYPES[dtype]))
+    ws = _attention_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.device(device), torch.cuda.stream(s):
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _attention_workspaces[key] = ws
+    return ws
+
+
+def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
+                         block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, scale: float,
+                         max_q_len: int, window: int = 0, sinks: int = 0, lse: Optional[torch.Tensor] = None,
+                         workspace_buf: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[T, q_heads, head_dim] = attention of each request's new tokens (rows
+    q_start[b] .. of q) over its cached ones, themselves included: causal, with
+    window > 0 only the last `window` keys and the first `sinks`. lse
+    (optional, fp32 [T, q_heads]): log of the weights' sum. max_q_len: the
+    largest number of new tokens of a request."""
+    dtype = q.dtype
+    q_p, q_s = _rows3(q, "q", dtype)
+    T, heads, D = q.shape
+    out_p, out_s = _rows3(out, "out", dtype, D)
+    pages, kv_heads, page, width = _cache(K_cache, V_cache, dtype)
+    if out.shape != q.shape or width != D:
+        raise ValueError("out, q and the cache must agree in heads and head_dim")
+    B = kv_len.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must have one row per request")
+    lse_p = None
+    if lse is not None:
+        if lse.shape != (T, heads):
+            raise ValueError("lse must be [T, q_heads]")
+        lse_p = _dev(lse, "lse", torch.float32)
+    ws = attention_workspace(q.device, D, dtype, stream) if workspace_buf is None else workspace_buf
+    st = lib.sgmv_paged_attention(out_p, out_s, lse_p, q_p, q_s, heads, K_cache.data_ptr(), V_cache.data_ptr(), pages,
+                                  kv_heads, page, D, _ints(block_table, "block_table"), block_table.shape[1],
+                                  _ints(q_start, "q_start", B + 1), _ints(kv_len, "kv_len"), B, T, max_q_len, scale,
+                                  window, sinks, _dtype_code(q), _dev(ws, "workspace"),
+                                  ws.numel() * ws.element_size(), _stream(q, stream))
+    _check("sgmv_paged_attention", st)
+    return out
+
+
 def sgmv_version() -> int:
     return int(lib.sgmv_version())
 
@@ -494,4 +672,6 @@ __all__ = ["sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_shrink_gather", "sg
            "sgmv_workspace_bytes", "sgmv_build_segments",
            "sgmv_pool_pointers", "sgmv_version", "workspace", "SGMVError", "lib", "EXPORTS",
            "LIBRARY", "SGMV_F32", "SGMV_BF16", "sgmv_workspace_status", "sgmv_set_wait_limit",
+           "sgmv_kv_tables", "sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "attention_workspace",
+           "SGMV_MAX_REQUESTS", "SGMV_ROPE_PLAIN", "SGMV_ROPE_LINEAR", "SGMV_ROPE_BY_PARTS",
            "SGMV_WS_WAIT_TIMEOUT", "SGMV_WS_BAD_OFFSETS", "sgmv_fused_noalloc", "SGMV_NOALLOC_SCRATCH_BYTES"]

@@ -3,8 +3,8 @@
 Usage: ``python segmented_gather_gemm_sgmv_amd/build.py``.
 
 The kernel file is compiled once per rank (-DSGMV_RANK=8, 16, 32, 64) and
-once more for the rank dispatch and helper kernels; these objects and the
-C ABI's compile in parallel, then link into one shared library.
+once more for the rank dispatch and helper kernels; these objects, the paged
+cache's and the C ABI's compile in parallel, then link into one shared library.
 """
 from __future__ import annotations
 
@@ -24,7 +24,8 @@ LIBRARY = PKG / "libsgmv.so"
 KERNELS = CSRC / "sgmv_kernels.hip"
 API = CSRC / "sgmv_api.cpp"
 HOST = CSRC / "sgmv_host.cpp"  # host-only entry points (no HIP): also built alone with the sanitizers
-SOURCES = [KERNELS, API, HOST]
+KV = [CSRC / "kv_api.cpp", CSRC / "kv_tables.hip", CSRC / "kv_rope.hip", CSRC / "kv_attention.hip"]  # the paged cache
+SOURCES = [KERNELS, API, HOST, *KV]
 RANKS = (8, 16, 32, 64)
 ARCH = "gfx950"
 
@@ -56,6 +57,7 @@ def build(output: Path = LIBRARY, extra_flags=(), verbose: bool = False, jobs: i
         units = [(KERNELS, [f"-DSGMV_RANK={r}"], Path(tmp) / f"kernels_r{r}.o") for r in RANKS]
         units += [(KERNELS, [], Path(tmp) / "kernels_dispatch.o"), (API, [], Path(tmp) / "api.o"),
                   (HOST, [], Path(tmp) / "host.o")]
+        units += [(src, [], Path(tmp) / f"{src.stem}.o") for src in KV]
         pending = list(units)
         running = []
         failed = []

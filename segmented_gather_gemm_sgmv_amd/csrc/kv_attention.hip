@@ -1,0 +1,413 @@
+// Attention of a step's new tokens over the paged key/value cache
+// (sgmv_paged_attention).
+//
+// Mathematics: per row, out = sum_j p_j V_j / sum_j p_j with
+// p_j = 2^(c s_j - c m), s_j = q . K_j, c = scale * log2 e, over one pass of
+// the keys: m is a running reference point, and the sums are multiplied by
+// 2^(c (m_old - m_new)) when it moves. It moves only when a score exceeds it
+// by more than kSlack in the exponent, since any reference point gives the
+// same quotient; weights then stay below 2^kSlack, which neither fp32 sums
+// nor bf16 weights lose anything by. The products are formed transposed,
+// S^T = K Q^T and O^T = V^T P^T, so that each lane holds one row's scores (the
+// row's maximum is a maximum over a lane's registers and two or one lane
+// swaps), the scores leave the first product in the layout in which the second
+// takes its weights, and the order of keys within a product is free.
+#include "kv_attention.h"
+#include "sgmv.h"
+
+namespace sgmv {
+
+namespace {
+
+using namespace attn;
+
+constexpr float kSlack = 8.f;
+
+// ----------------------------------------------------------------------------
+// Streaming kernel: groups of few rows (decode, and every fp32 batch).
+//
+// What bounds it: HBM; a group reads its keys and values once. A workgroup
+// takes one item, its four waves every fourth key tile, each with its own
+// running softmax; the four results meet in LDS at the end. A wave's tile
+// (32 keys in bf16, 16 in fp32: 8 KB of K and of V at head_dim 128) is loaded
+// row-contiguously into registers while the previous one is worked on, then
+// goes through the wave's own LDS region into the matrix instructions' layout,
+// with no barrier in the loop. 16 rows go through v_mfma_*_16x16: with fewer
+// rows the rest of the tile is idle, which costs nothing that HBM would not.
+// ----------------------------------------------------------------------------
+constexpr int kStreamRows = 16;
+constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
+constexpr int kStreamMinChunk = 16;  // key tiles a split has at least (four per wave)
+
+template <typename T, int D>
+struct Stream {
+    static constexpr bool kBf16 = Elem<T>::kPerVec == 8;
+    static constexpr int kBlocks = kBf16 ? 2 : 1;     // 16-key blocks per tile
+    static constexpr int kKeys = 16 * kBlocks;
+    static constexpr int kChunks = D / Elem<T>::kPerVec;  // 16-byte chunks per row
+    static constexpr int kLoads = 16 * kChunks / 64;  // loads per lane and 16-key block
+    static constexpr int kTileBytes = kKeys * kChunks * 16;
+    static constexpr int kOut = D / 16;               // 16-column blocks of the output
+    static constexpr int kOutStride = D + 4;          // floats per row of the waves' results in LDS
+    static constexpr int kLdsBytes = kWaves * 2 * kTileBytes > kWaves * 16 * kOutStride * 4
+                                         ? kWaves * 2 * kTileBytes
+                                         : kWaves * 16 * kOutStride * 4;
+    static constexpr int kSlotFloats = 16 * D + 32;   // partial result: 16 x D sums, 16 maxima, 16 weight sums
+
+    // Chunk c of row r sits in chunk slot c ^ swizzle(r): the 16 rows that one
+    // K read takes at one chunk index, and the 4 or 8 rows of one V read, lie
+    // in different banks.
+    static __device__ __forceinline__ int k_slot(int row, int c) {
+        const int x = kChunks >= 16 ? row & 15 : (row >> 1) & 7;
+        return row * kChunks + (c ^ x);
+    }
+    static __device__ __forceinline__ int v_slot(int row, int c) {
+        int x;
+        if (!kBf16)
+            x = 4 * ((row >> 2) & 3);
+        else if (kChunks >= 16)
+            x = 4 * (row & 3) + 2 * ((row >> 2) & 1);
+        else
+            x = 4 * ((row >> 1) & 1) + 2 * ((row >> 2) & 1);
+        return row * kChunks + (c ^ x);
+    }
+};
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(float a, float b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// LDS operations of one wave complete in order; this only keeps the compiler
+// from moving them across.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+// Four rows' values of one column per lane: lane i of a 16-lane group gives
+// the address of four columns of row i / 4 and receives column i of the four
+// rows.
+__device__ __forceinline__ s16x4_t read_transposed(const void *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)p);
+}
+
+// Writes one row's result: sum / weight, rounded once, and the log-sum-exp.
+template <typename T>
+__device__ __forceinline__ void store_row4(const AttnArgs &a, int64_t row, int head, int d, f32x4_t sum, float weight) {
+    const float inv = weight > 0.f || weight != weight ? 1.f / weight : 0.f;
+    const f32x4_t o = sum * inv;
+    T *dst = static_cast<T *>(a.out) + row * a.out_stride + (int64_t)head * a.head_dim + d;
+    if constexpr (Elem<T>::kPerVec == 8) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    } else {
+        *reinterpret_cast<float4 *>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+__device__ __forceinline__ float lse_of(float m, float weight) {
+    return weight > 0.f || weight != weight ? m * kLn2 + logf(weight) : kNone;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
+                                                             float *slots) {
+    using S = Stream<T, D>;
+    constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
+    __shared__ __align__(16) unsigned char lds[S::kLdsBytes];
+    __shared__ PlanSmem plan;
+    __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+    __shared__ int s_flag;
+
+    Item it;
+    if (!find_item<kStreamRows, S::kKeys>(a, take, short_rows, kStreamTarget, kStreamMinChunk, blockIdx.x, gridDim.x,
+                                          plan, it))
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
+    const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
+    const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
+    const int pa = it.p0 + tok_a, pb = it.p0 + tok_b;
+    const TileRun run = tile_run<S::kKeys>(pa, pb, a.window, a.sinks);
+    const int splits = max((run.count + it.chunk - 1) / it.chunk, 1);
+    if (it.split >= splits) return;
+    const int t1 = min(run.count, (it.split + 1) * it.chunk);
+
+    // This lane's row: query fragments, position, first key of its window.
+    const int my = row0 + r, tok = my / a.group;
+    const bool valid = my < rows;
+    const int q_head = it.head * a.group + my % a.group;
+    const int pos = valid ? it.p0 + tok : -1;
+    const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
+    const int nch = a.head_dim / Elem<T>::kPerVec;
+    uint4 qf[CH / 4];
+    {
+        const T *q = static_cast<const T *>(a.q) + (int64_t)(it.q0 + (valid ? tok : 0)) * a.q_stride +
+                     (int64_t)(valid ? q_head : 0) * a.head_dim;
+#pragma unroll
+        for (int k = 0; k < CH / 4; ++k) {
+            const int c = 4 * k + g;
+            const uint4 v = ld16(q + (c < nch ? c : 0) * Elem<T>::kPerVec);
+            qf[k] = valid && c < nch ? v : make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    unsigned char *k_lds = lds + wave * 2 * S::kTileBytes, *v_lds = k_lds + S::kTileBytes;
+    if (nch < CH) {  // a narrower head: the chunks past it stay zero
+        for (int i = lane; i < 2 * S::kTileBytes / 16; i += 64)
+            reinterpret_cast<uint4 *>(k_lds)[i] = make_uint4(0, 0, 0, 0);
+        wave_lds_order();
+    }
+
+    // Pages of this wave's next 64 16-key blocks, one per lane.
+    const int row_bytes = a.head_dim * (int)sizeof(T);
+    const int page_mask = (1 << a.page_shift) - 1;
+    int pages = 0;
+    const int first = it.split * it.chunk + wave;
+    auto load_pages = [&](int i) {  // the wave's tiles i, i + 1, ...
+        const int v = first + kWaves * (i + lane / NB);
+        pages = 0;
+        if (v < t1) {
+            const int key = run.tile(v) * S::kKeys + 16 * (lane % NB), at = key >> a.page_shift;
+            if (at < a.max_blocks) {
+                const int p = a.block_table[(int64_t)it.b * a.max_blocks + at];
+                pages = (unsigned)p < (unsigned)a.num_pages ? p : 0;
+            }
+        }
+    };
+    uint4 kr[NB * NL], vr[NB * NL];
+    auto load_tile = [&](int i, int v) {
+        const int key0 = run.tile(v) * S::kKeys;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int page = __builtin_amdgcn_readlane(pages, (i % (64 / NB)) * NB + nb);
+            const int64_t row = (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + ((key0 + 16 * nb) & page_mask);
+            const char *kp = static_cast<const char *>(a.K) + row * row_bytes;
+            const char *vp = static_cast<const char *>(a.V) + row * row_bytes;
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int f = j * 64 + lane, c = f % CH;
+                const uint32_t off = (uint32_t)(f / CH * row_bytes + (c < nch ? c : 0) * 16);
+                kr[nb * NL + j] = ld16(kp + off);
+                vr[nb * NL + j] = ld16(vp + off);
+            }
+        }
+    };
+
+    const float c2 = a.scale * kLog2e;
+    float m = kNone, l = 0.f;  // m in units of scale * log2 e
+    f32x4_t o[S::kOut];
+#pragma unroll
+    for (int d = 0; d < S::kOut; ++d) o[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    load_pages(0);
+    if (first < t1) load_tile(0, first);
+    for (int i = 0, v = first; v < t1; ++i, v += kWaves) {
+        const int key0 = run.tile(v) * S::kKeys;
+        // Every row of the tile sees every key.
+        const bool whole = key0 + S::kKeys - 1 <= pa && (pb_lo <= key0 || key0 + S::kKeys <= a.sinks);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int f = j * 64 + lane, row = 16 * nb + f / CH, c = f % CH, key = key0 + row;
+                uint4 vv = vr[nb * NL + j];
+                // Values of keys that no row sees meet zero weights, which a NaN would survive.
+                if (!whole && (key > pb || (key < pa_lo && key >= a.sinks))) vv = make_uint4(0, 0, 0, 0);
+                if (c < nch) {
+                    reinterpret_cast<uint4 *>(k_lds)[S::k_slot(row, c)] = kr[nb * NL + j];
+                    reinterpret_cast<uint4 *>(v_lds)[S::v_slot(row, c)] = vv;
+                }
+            }
+        wave_lds_order();
+        if (v + kWaves < t1) {
+            if ((i + 1) % (64 / NB) == 0) load_pages(i + 1);
+            load_tile(i + 1, v + kWaves);
+        }
+
+        f32x4_t s[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            s[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < CH / 4; ++k) {
+                const uint4 kf = reinterpret_cast<const uint4 *>(k_lds)[S::k_slot(16 * nb + r, 4 * k + g)];
+                if constexpr (S::kBf16) {
+                    s[nb] = mfma16(__builtin_bit_cast(bf16x8_t, kf), __builtin_bit_cast(bf16x8_t, qf[k]), s[nb]);
+                } else {
+                    s[nb] = mfma16(__uint_as_float(kf.x), __uint_as_float(qf[k].x), s[nb]);
+                    s[nb] = mfma16(__uint_as_float(kf.y), __uint_as_float(qf[k].y), s[nb]);
+                    s[nb] = mfma16(__uint_as_float(kf.z), __uint_as_float(qf[k].z), s[nb]);
+                    s[nb] = mfma16(__uint_as_float(kf.w), __uint_as_float(qf[k].w), s[nb]);
+                }
+            }
+        }
+        if (!whole) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + 16 * nb + 4 * g + e;
+                    const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+                    s[nb][e] = seen ? s[nb][e] : kNone;
+                }
+        }
+        float top = kNone;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, s[nb][e]);
+        top = swap32_max(swap16_max(top)) * c2;
+        if (__any(top > m + kSlack || (m == kNone && top > kNone))) {
+            const float to = fmaxf(m, top);
+            const float keep = exp2_fast(m - ref_of(to));
+            l *= keep;
+#pragma unroll
+            for (int d = 0; d < S::kOut; ++d) o[d] *= keep;
+            m = to;
+        }
+        const float ref = ref_of(m);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nb][e] = exp2_fast(__builtin_fmaf(s[nb][e], c2, -ref));
+                l += s[nb][e];
+            }
+
+        if constexpr (S::kBf16) {
+            // Weight slots 8 g + j of this lane: keys 4 g + j (j < 4) and 16 + 4 g + j - 4.
+            const uint4 pw = make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                                        pack_bf16x2(s[NB - 1][0], s[NB - 1][1]),
+                                        pack_bf16x2(s[NB - 1][2], s[NB - 1][3]));
+            const bf16x8_t p = __builtin_bit_cast(bf16x8_t, pw);
+            const int row = 4 * g + (r >> 2), half = 8 * (r & 1);
+#pragma unroll
+            for (int d = 0; d < S::kOut; ++d) {
+                const int c = 2 * d + ((r & 3) >> 1);
+                union {
+                    s16x4_t h[2];
+                    bf16x8_t v;
+                } vf;
+                vf.h[0] = read_transposed(v_lds + S::v_slot(row, c) * 16 + half);
+                vf.h[1] = read_transposed(v_lds + S::v_slot(row + 16, c) * 16 + half);
+                o[d] = mfma16(vf.v, p, o[d]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int d = 0; d < S::kOut; ++d) {
+                    const float *vp = reinterpret_cast<const float *>(v_lds + S::v_slot(4 * g + e, 4 * d + (r >> 2)) * 16);
+                    o[d] = mfma16(vp[r & 3], s[0][e], o[d]);
+                }
+        }
+        wave_lds_order();
+    }
+
+    // The four waves' results meet in LDS, in wave order.
+    l = swap32_sum(swap16_sum(l));
+    if (g == 0) {
+        s_m[wave][r] = m;
+        s_l[wave][r] = l;
+    }
+    __syncthreads();
+    const float m_all = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+    const float keep = exp2_fast(m - ref_of(m_all));
+    float *o_lds = reinterpret_cast<float *>(lds) + (wave * 16 + r) * S::kOutStride;
+#pragma unroll
+    for (int d = 0; d < S::kOut; ++d) *reinterpret_cast<f32x4_t *>(o_lds + 16 * d + 4 * g) = o[d] * keep;
+    __syncthreads();
+
+    const __amdgpu_buffer_rsrc_t part =
+        part_rsrc(slots + (int64_t)it.first_slot * S::kSlotFloats, (uint32_t)splits * S::kSlotFloats * 4);
+    const int live = min(kStreamRows, rows - row0);
+    const int vecs = a.head_dim / 4;  // 4-column pieces of a row
+    for (int e = tid; e < live * vecs; e += kThreads) {
+        const int row = e / vecs, d = e % vecs * 4;
+        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        float top = kNone, weight = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w][row]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            sum += *reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(lds) +
+                                                      (w * 16 + row) * S::kOutStride + d);
+            weight += s_l[w][row] * exp2_fast(s_m[w][row] - ref_of(top));
+        }
+        if (splits == 1) {
+            const int at = row0 + row, head = it.head * a.group + at % a.group;
+            const int64_t q_row = it.q0 + at / a.group;
+            store_row4<T>(a, q_row, head, d, sum, weight);
+            if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
+        } else {
+            const uint32_t slot = (uint32_t)it.split * S::kSlotFloats * 4;
+            part_store(part, slot + (row * D + d) * 4, sum);
+            if (d == 0) {
+                part_store1(part, slot + (16 * D + row) * 4, top);
+                part_store1(part, slot + (16 * D + 16 + row) * 4, weight);
+            }
+        }
+    }
+    if (splits == 1) return;
+
+    // The last of the group's items to arrive adds the splits up, in their order.
+    uint32_t *counter = counters + it.first_slot;
+    if (!arrive_last(counter, (uint32_t)splits, &s_flag)) return;
+    for (int e = tid; e < live * vecs; e += kThreads) {
+        const int row = e / vecs, d = e % vecs * 4;
+        float top = kNone;
+        for (int k = 0; k < splits; ++k)
+            top = fmaxf(top, part_load1(part, ((uint32_t)k * S::kSlotFloats + 16 * D + row) * 4));
+        const float ref = ref_of(top);
+        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        float weight = 0.f;
+        for (int k = 0; k < splits; ++k) {
+            const uint32_t slot = (uint32_t)k * S::kSlotFloats;
+            const float keep_k = exp2_fast(part_load1(part, (slot + 16 * D + row) * 4) - ref);
+            weight += keep_k * part_load1(part, (slot + 16 * D + 16 + row) * 4);
+            sum += part_load(part, (slot + row * D + d) * 4) * keep_k;
+        }
+        const int at = row0 + row, head = it.head * a.group + at % a.group;
+        const int64_t q_row = it.q0 + at / a.group;
+        store_row4<T>(a, q_row, head, d, sum, weight);
+        if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
+    }
+    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+constexpr size_t kCounterBytes = (size_t)2 * kStreamTarget * sizeof(uint32_t);
+
+template <typename T, int D>
+hipError_t launch_stream(const AttnArgs &a, int take, int short_rows, int64_t groups, hipStream_t st) {
+    const int64_t grid = groups * a.kv_heads + kStreamTarget;
+    if (grid > (int64_t)1 << 24) return hipErrorInvalidValue;
+    char *ws = static_cast<char *>(a.workspace);
+    hipLaunchKernelGGL((stream_kernel<T, D>), dim3((unsigned)grid), dim3(kThreads), 0, st, a, take, short_rows,
+                       reinterpret_cast<uint32_t *>(ws), reinterpret_cast<float *>(ws + kCounterBytes));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(int head_dim, int) {
+    const int d = head_dim <= 64 ? 64 : 128;
+    return kCounterBytes + (size_t)2 * kStreamTarget * (16 * d + 32) * sizeof(float);
+}
+
+hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
+    const int64_t per = ((int64_t)a.max_q_len * a.group + kStreamRows - 1) / kStreamRows;
+    const int64_t by_rows = (int64_t)a.T * a.group / kStreamRows + a.num_requests;
+    const int64_t groups = per * a.num_requests < by_rows ? per * a.num_requests : by_rows;
+    if (a.dtype == SGMV_BF16)
+        return a.head_dim <= 64 ? launch_stream<bf16_t, 64>(a, kTakeAll, 0, groups, st)
+                                : launch_stream<bf16_t, 128>(a, kTakeAll, 0, groups, st);
+    return a.head_dim <= 64 ? launch_stream<float, 64>(a, kTakeAll, 0, groups, st)
+                            : launch_stream<float, 128>(a, kTakeAll, 0, groups, st);
+}
+
+}  // namespace sgmv
