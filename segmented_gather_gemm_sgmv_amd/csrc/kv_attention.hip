@@ -380,34 +380,330 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-constexpr size_t kCounterBytes = (size_t)2 * kStreamTarget * sizeof(uint32_t);
+// ----------------------------------------------------------------------------
+// Tile kernel: bf16 groups of many rows (prompt chunks).
+//
+// What bounds it: the matrix cores. A workgroup takes 128 packed rows, 32 per
+// wave, against key tiles of 64 that its waves share: the next tile is loaded
+// into registers while the present one is worked on from LDS, then written to
+// the other of two LDS buffers, one barrier per tile. 32 rows go through
+// v_mfma_f32_32x32x16_bf16, whose transposed scores leave half of a row's keys
+// on each of two lanes.
+// ----------------------------------------------------------------------------
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 64;
+constexpr int kTileTarget = 512;   // as kStreamTarget
+constexpr int kTileMinChunk = 8;   // key tiles a split has at least
+constexpr int kShortRows = 16;     // groups up to this many rows go to the streaming kernel
 
-template <typename T, int D>
-hipError_t launch_stream(const AttnArgs &a, int take, int short_rows, int64_t groups, hipStream_t st) {
-    const int64_t grid = groups * a.kv_heads + kStreamTarget;
+template <int D>
+struct Tile {
+    static constexpr int kChunks = D / 8;
+    static constexpr int kLoads = kTileKeys * kChunks / kThreads;  // per thread, of K and of V
+    static constexpr int kBytes = kTileKeys * kChunks * 16;
+    static constexpr int kOut = D / 32;                            // 32-column blocks of the output
+    static constexpr int kSlotFloats = kTileRows * D + 2 * kTileRows;
+};
+
+__device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
+                                                           float *slots) {
+    using L = Tile<D>;
+    using S = Stream<bf16_t, D>;  // the LDS layouts of a row
+    constexpr int CH = L::kChunks, NL = L::kLoads;
+    __shared__ __align__(16) unsigned char lds[2][2][L::kBytes];  // buffer, K / V
+    __shared__ PlanSmem plan;
+    __shared__ int s_flag;
+
+    Item it;
+    if (!find_item<kTileRows, kTileKeys>(a, take, short_rows, kTileTarget, kTileMinChunk, blockIdx.x, gridDim.x, plan,
+                                         it))
+        return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
+    const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
+    const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
+    const TileRun run = tile_run<kTileKeys>(pa, pb, a.window, a.sinks);
+    const int splits = max((run.count + it.chunk - 1) / it.chunk, 1);
+    if (it.split >= splits) return;
+    const int t0 = it.split * it.chunk, t1 = min(run.count, t0 + it.chunk);
+
+    const int wrow = row0 + 32 * wave;  // this wave's rows; past the last row it only helps loading
+    const bool live_wave = wrow < rows;
+    const int wa = it.p0 + wrow / a.group, wb = it.p0 + (min(wrow + 32, rows) - 1) / a.group;
+    const int my = wrow + r, tok = my / a.group;
+    const bool valid = my < rows;
+    const int q_head = it.head * a.group + my % a.group;
+    const int pos = valid ? it.p0 + tok : -1;
+    const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0;
+    const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
+    const int nch = a.head_dim / 8;
+    bf16x8_t qf[CH / 2];
+    {
+        const bf16_t *q = static_cast<const bf16_t *>(a.q) + (int64_t)(it.q0 + (valid ? tok : 0)) * a.q_stride +
+                          (int64_t)(valid ? q_head : 0) * a.head_dim;
+#pragma unroll
+        for (int k = 0; k < CH / 2; ++k) {
+            const int c = 2 * k + h;
+            const uint4 v = ld16(q + (c < nch ? c : 0) * 8);
+            qf[k] = __builtin_bit_cast(bf16x8_t, valid && c < nch ? v : make_uint4(0, 0, 0, 0));
+        }
+    }
+    if (nch < CH) {  // a narrower head: the chunks past it stay zero
+        for (int i = tid; i < 4 * L::kBytes / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(lds)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+
+    const int row_bytes = a.head_dim * 2, page_mask = (1 << a.page_shift) - 1;
+    int pages = 0;  // of the next 16 tiles' 64 16-key blocks, one per lane
+    auto load_pages = [&](int i) {
+        const int v = t0 + i + lane / 4;
+        pages = 0;
+        if (v < t1) {
+            const int at = (run.tile(v) * kTileKeys + 16 * (lane % 4)) >> a.page_shift;
+            if (at < a.max_blocks) {
+                const int p = a.block_table[(int64_t)it.b * a.max_blocks + at];
+                pages = (unsigned)p < (unsigned)a.num_pages ? p : 0;
+            }
+        }
+    };
+    uint4 kr[NL], vr[NL];
+    auto load_tile = [&](int i) {
+        const int key0 = run.tile(t0 + i) * kTileKeys;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int f = j * kThreads + tid, c = f % CH;
+            const int block = __builtin_amdgcn_readfirstlane(f / CH / 16);  // a wave's chunks lie in one block
+            const int page = __builtin_amdgcn_readlane(pages, i % 16 * 4 + block);
+            const int64_t row =
+                (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + ((key0 + 16 * block) & page_mask);
+            const uint32_t off = (uint32_t)(f / CH % 16 * row_bytes + (c < nch ? c : 0) * 16);
+            kr[j] = ld16(static_cast<const char *>(a.K) + row * row_bytes + off);
+            vr[j] = ld16(static_cast<const char *>(a.V) + row * row_bytes + off);
+        }
+    };
+    auto write_tile = [&](int i) {
+        const int key0 = run.tile(t0 + i) * kTileKeys;
+        uint4 *kb = reinterpret_cast<uint4 *>(lds[i & 1][0]), *vb = reinterpret_cast<uint4 *>(lds[i & 1][1]);
+        const bool whole = key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int f = j * kThreads + tid, c = f % CH, row = f / CH, key = key0 + row;
+            uint4 vv = vr[j];
+            // Values of keys that no row sees meet zero weights, which a NaN would survive.
+            if (!whole && (key > pb || (key < pa_lo && key >= a.sinks))) vv = make_uint4(0, 0, 0, 0);
+            if (c < nch) {
+                kb[S::k_slot(row, c)] = kr[j];
+                vb[S::v_slot(row, c)] = vv;
+            }
+        }
+    };
+
+    const float c2 = a.scale * kLog2e;
+    float m = kNone, l = 0.f;
+    f32x16_t o[L::kOut];
+#pragma unroll
+    for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+
+    const int n = t1 - t0;
+    if (n > 0) {
+        load_pages(0);
+        load_tile(0);
+        write_tile(0);
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+        if (i + 1 < n) {
+            if ((i + 1) % 16 == 0) load_pages(i + 1);
+            load_tile(i + 1);
+        }
+        const int key0 = run.tile(t0 + i) * kTileKeys;
+        const uint4 *kb = reinterpret_cast<const uint4 *>(lds[i & 1][0]);
+        const unsigned char *vb = lds[i & 1][1];
+        const bool any = live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks);
+        if (any) {
+            f32x16_t s[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < CH / 2; ++k)
+                    s[b] = mfma32(__builtin_bit_cast(bf16x8_t, kb[S::k_slot(32 * b + r, 2 * k + h)]), qf[k], s[b]);
+            }
+            if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int key = key0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
+                        const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+                        s[b][e] = seen ? s[b][e] : kNone;
+                    }
+            }
+            float top = kNone;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+            top = swap32_max(top) * c2;
+            if (__any(top > m + kSlack)) {
+                const float to = fmaxf(m, top);
+                const float keep = exp2_fast(m - ref_of(to));
+                l *= keep;
+#pragma unroll
+                for (int d = 0; d < L::kOut; ++d) o[d] *= keep;
+                m = to;
+            }
+            const float ref = ref_of(m);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[b][e] = exp2_fast(__builtin_fmaf(s[b][e], c2, -ref));
+                    l += s[b][e];
+                }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
+                const f32x16_t &w = s[t / 2];
+                const int e = t % 2 * 8;
+                const bf16x8_t p = __builtin_bit_cast(
+                    bf16x8_t, make_uint4(pack_bf16x2(w[e], w[e + 1]), pack_bf16x2(w[e + 2], w[e + 3]),
+                                         pack_bf16x2(w[e + 4], w[e + 5]), pack_bf16x2(w[e + 6], w[e + 7])));
+                const int row = 16 * t + 4 * h + ((lane & 15) >> 2), half = 8 * (lane & 1);
+#pragma unroll
+                for (int d = 0; d < L::kOut; ++d) {
+                    const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+                    union {
+                        s16x4_t x[2];
+                        bf16x8_t v;
+                    } vf;
+                    vf.x[0] = read_transposed(vb + S::v_slot(row, c) * 16 + half);
+                    vf.x[1] = read_transposed(vb + S::v_slot(row + 8, c) * 16 + half);
+                    o[d] = mfma32(vf.v, p, o[d]);
+                }
+            }
+        }
+        if (i + 1 < n) write_tile(i + 1);
+        __syncthreads();
+    }
+
+    l = swap32_sum(l);
+    const __amdgpu_buffer_rsrc_t part =
+        part_rsrc(slots + (int64_t)it.first_slot * L::kSlotFloats, (uint32_t)splits * L::kSlotFloats * 4);
+    if (valid) {
+        const int64_t q_row = it.q0 + tok;
+        const uint32_t slot = (uint32_t)it.split * L::kSlotFloats * 4;
+        const int row = 32 * wave + r;
+#pragma unroll
+        for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int at = 32 * d + 2 * e + 4 * h;
+                const f32x4_t x = {o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
+                if (at >= a.head_dim) continue;
+                if (splits == 1)
+                    store_row4<bf16_t>(a, q_row, q_head, at, x, l);
+                else
+                    part_store(part, slot + (row * D + at) * 4, x);
+            }
+        if (h == 0) {
+            if (splits == 1) {
+                if (a.lse) a.lse[q_row * a.q_heads + q_head] = lse_of(m, l);
+            } else {
+                part_store1(part, slot + (kTileRows * D + row) * 4, m);
+                part_store1(part, slot + (kTileRows * D + kTileRows + row) * 4, l);
+            }
+        }
+    }
+    if (splits == 1) return;
+
+    // The last of the group's items to arrive adds the splits up, in their order.
+    uint32_t *counter = counters + it.first_slot;
+    if (!arrive_last(counter, (uint32_t)splits, &s_flag)) return;
+    const int live = min(kTileRows, rows - row0), vecs = a.head_dim / 4;
+    for (int e = tid; e < live * vecs; e += kThreads) {
+        const int row = e / vecs, d = e % vecs * 4;
+        float top = kNone;
+        for (int k = 0; k < splits; ++k)
+            top = fmaxf(top, part_load1(part, ((uint32_t)k * L::kSlotFloats + kTileRows * D + row) * 4));
+        const float ref = ref_of(top);
+        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        float weight = 0.f;
+        for (int k = 0; k < splits; ++k) {
+            const uint32_t slot = (uint32_t)k * L::kSlotFloats;
+            const float keep = exp2_fast(part_load1(part, (slot + kTileRows * D + row) * 4) - ref);
+            weight += keep * part_load1(part, (slot + kTileRows * D + kTileRows + row) * 4);
+            sum += part_load(part, (slot + row * D + d) * 4) * keep;
+        }
+        const int at = row0 + row, head = it.head * a.group + at % a.group;
+        const int64_t q_row = it.q0 + at / a.group;
+        store_row4<bf16_t>(a, q_row, head, d, sum, weight);
+        if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
+    }
+    if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// ----------------------------------------------------------------------------
+// Launches and workspace
+// ----------------------------------------------------------------------------
+constexpr int kMaxSlots = 2 * (kStreamTarget > kTileTarget ? kStreamTarget : kTileTarget);
+constexpr size_t kCounterBytes = (size_t)kMaxSlots * sizeof(uint32_t);
+
+// The most groups of `rows` packed rows that requests of up to max_q_len
+// tokens, T in all, can make: every request's last group may be part full.
+int64_t most_groups(const AttnArgs &a, int64_t requests, int rows) {
+    const int64_t per = ((int64_t)a.max_q_len * a.group + rows - 1) / rows;
+    const int64_t by_rows = (int64_t)a.T * a.group / rows + requests;
+    return per * requests < by_rows ? per * requests : by_rows;
+}
+
+template <typename Kernel>
+hipError_t launch(Kernel kernel, const AttnArgs &a, int take, int64_t groups, int target, hipStream_t st) {
+    const int64_t grid = groups * a.kv_heads + target;
     if (grid > (int64_t)1 << 24) return hipErrorInvalidValue;
     char *ws = static_cast<char *>(a.workspace);
-    hipLaunchKernelGGL((stream_kernel<T, D>), dim3((unsigned)grid), dim3(kThreads), 0, st, a, take, short_rows,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, a, take, kShortRows,
                        reinterpret_cast<uint32_t *>(ws), reinterpret_cast<float *>(ws + kCounterBytes));
     return hipGetLastError();
 }
 
+template <typename T>
+hipError_t launch_stream(const AttnArgs &a, int take, int64_t groups, hipStream_t st) {
+    return a.head_dim <= 64 ? launch(stream_kernel<T, 64>, a, take, groups, kStreamTarget, st)
+                            : launch(stream_kernel<T, 128>, a, take, groups, kStreamTarget, st);
+}
+
 }  // namespace
 
-size_t attention_workspace_bytes(int head_dim, int) {
-    const int d = head_dim <= 64 ? 64 : 128;
-    return kCounterBytes + (size_t)2 * kStreamTarget * (16 * d + 32) * sizeof(float);
+size_t attention_workspace_bytes(int head_dim, int dtype) {
+    const size_t d = head_dim <= 64 ? 64 : 128;
+    const size_t stream = 2 * kStreamTarget * (kStreamRows * d + 2 * kStreamRows);
+    const size_t tile = dtype == SGMV_BF16 ? 2 * kTileTarget * (kTileRows * d + 2 * kTileRows) : 0;
+    return kCounterBytes + (stream > tile ? stream : tile) * sizeof(float);
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-    const int64_t per = ((int64_t)a.max_q_len * a.group + kStreamRows - 1) / kStreamRows;
-    const int64_t by_rows = (int64_t)a.T * a.group / kStreamRows + a.num_requests;
-    const int64_t groups = per * a.num_requests < by_rows ? per * a.num_requests : by_rows;
-    if (a.dtype == SGMV_BF16)
-        return a.head_dim <= 64 ? launch_stream<bf16_t, 64>(a, kTakeAll, 0, groups, st)
-                                : launch_stream<bf16_t, 128>(a, kTakeAll, 0, groups, st);
-    return a.head_dim <= 64 ? launch_stream<float, 64>(a, kTakeAll, 0, groups, st)
-                            : launch_stream<float, 128>(a, kTakeAll, 0, groups, st);
+    if (a.dtype != SGMV_BF16) return launch_stream<float>(a, kTakeAll, most_groups(a, a.num_requests, kStreamRows), st);
+    // A batch whose requests all fit one row tile of the streaming kernel is its alone.
+    if ((int64_t)a.max_q_len * a.group <= kShortRows) return launch_stream<bf16_t>(a, kTakeAll, a.num_requests, st);
+    // Otherwise requests go to the two kernels by their rows. At most T * group / (kShortRows + 1) of them are long.
+    const int64_t could = (int64_t)a.T * a.group / (kShortRows + 1);
+    const bool one = a.num_requests == 1;
+    const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
+    const int64_t groups = most_groups(a, longs, kTileRows);
+    const int take = one ? kTakeAll : kTakeLong;
+    const hipError_t e = a.head_dim <= 64 ? launch(tile_kernel<64>, a, take, groups, kTileTarget, st)
+                                          : launch(tile_kernel<128>, a, take, groups, kTileTarget, st);
+    if (e != hipSuccess || one) return e;
+    return launch_stream<bf16_t>(a, kTakeShort, a.num_requests, st);
 }
 
 }  // namespace sgmv
