@@ -409,6 +409,21 @@ __device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ bf16x8_t read_row(uint32_t at) {
+    return *(const __attribute__((address_space(3))) bf16x8_t *)(uintptr_t)at;
+}
+
+// Eight rows' values of one column per lane: rows of `at` and `step` past it.
+__device__ __forceinline__ bf16x8_t read_columns(uint32_t at, uint32_t step) {
+    union {
+        s16x4_t x[2];
+        bf16x8_t v;
+    } f;
+    f.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(uintptr_t)at);
+    f.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(uintptr_t)(at + step));
+    return f.v;
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
                                                            float *slots) {
@@ -490,16 +505,20 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     auto write_tile = [&](int i) {
         const int key0 = run.tile(t0 + i) * kTileKeys;
         uint4 *kb = reinterpret_cast<uint4 *>(lds[i & 1][0]), *vb = reinterpret_cast<uint4 *>(lds[i & 1][1]);
-        const bool whole = key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks);
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int f = j * kThreads + tid, c = f % CH, row = f / CH, key = key0 + row;
-            uint4 vv = vr[j];
+        if (!(key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
             // Values of keys that no row sees meet zero weights, which a NaN would survive.
-            if (!whole && (key > pb || (key < pa_lo && key >= a.sinks))) vv = make_uint4(0, 0, 0, 0);
-            if (c < nch) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int key = key0 + (j * kThreads + tid) / CH;
+                if (key > pb || (key < pa_lo && key >= a.sinks)) vr[j] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (tid % CH < nch) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int f = j * kThreads + tid, c = f % CH, row = f / CH;
                 kb[S::k_slot(row, c)] = kr[j];
-                vb[S::v_slot(row, c)] = vv;
+                vb[S::v_slot(row, c)] = vr[j];
             }
         }
     };
@@ -511,6 +530,14 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+
+    // LDS addresses of this lane's fragments; the others of a tile differ from them by one exclusive or (the chunk)
+    // and a constant (the rows), which the swizzles leave alone.
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)&lds[0][0][0];
+    const uint32_t k_at = lds_at + S::k_slot(r, h) * 16;
+    const int v_row = 4 * h + ((lane & 15) >> 2);
+    const uint32_t v_at =
+        lds_at + L::kBytes + S::v_slot(v_row, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) * 16 + 8 * (lane & 1);
 
     const int n = t1 - t0;
     if (n > 0) {
@@ -525,26 +552,42 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
             load_tile(i + 1);
         }
         const int key0 = run.tile(t0 + i) * kTileKeys;
-        const uint4 *kb = reinterpret_cast<const uint4 *>(lds[i & 1][0]);
-        const unsigned char *vb = lds[i & 1][1];
+        const uint32_t buf = (i & 1) * 2 * L::kBytes;
         const bool any = live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks);
         if (any) {
+            // K fragments of the second 32 keys are read while the first 32's products run.
+            bf16x8_t kf[2][CH / 2];
+#pragma unroll
+            for (int k = 0; k < CH / 2; ++k) kf[0][k] = read_row((k_at ^ (k * 32)) + buf);
+            __builtin_amdgcn_sched_barrier(0);
             f32x16_t s[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-                for (int k = 0; k < CH / 2; ++k)
-                    s[b] = mfma32(__builtin_bit_cast(bf16x8_t, kb[S::k_slot(32 * b + r, 2 * k + h)]), qf[k], s[b]);
+            for (int k = 0; k < CH / 2; ++k) {
+                kf[1][k] = read_row((k_at ^ (k * 32)) + buf + 32 * CH * 16);
+                s[0] = mfma32(kf[0][k], qf[k], s[0]);
             }
+#pragma unroll
+            for (int k = 0; k < CH / 2; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read,
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < CH / 2; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
+            bf16x8_t vf[2][L::kOut];  // V fragments of two 16-key steps
+#pragma unroll
+            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns((v_at ^ (d * 64)) + buf, 8 * CH * 16);
             if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int key = key0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
-                        const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+                        const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
                         s[b][e] = seen ? s[b][e] : kNone;
                     }
             }
@@ -564,31 +607,24 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
             }
             const float ref = ref_of(m);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    s[b][e] = exp2_fast(__builtin_fmaf(s[b][e], c2, -ref));
-                    l += s[b][e];
-                }
-#pragma unroll
             for (int t = 0; t < 4; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
-                const f32x16_t &w = s[t / 2];
-                const int e = t % 2 * 8;
-                const bf16x8_t p = __builtin_bit_cast(
-                    bf16x8_t, make_uint4(pack_bf16x2(w[e], w[e + 1]), pack_bf16x2(w[e + 2], w[e + 3]),
-                                         pack_bf16x2(w[e + 4], w[e + 5]), pack_bf16x2(w[e + 6], w[e + 7])));
-                const int row = 16 * t + 4 * h + ((lane & 15) >> 2), half = 8 * (lane & 1);
+                float w[8];
 #pragma unroll
-                for (int d = 0; d < L::kOut; ++d) {
-                    const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-                    union {
-                        s16x4_t x[2];
-                        bf16x8_t v;
-                    } vf;
-                    vf.x[0] = read_transposed(vb + S::v_slot(row, c) * 16 + half);
-                    vf.x[1] = read_transposed(vb + S::v_slot(row + 8, c) * 16 + half);
-                    o[d] = mfma32(vf.v, p, o[d]);
+                for (int e = 0; e < 8; ++e) {
+                    w[e] = exp2_fast(__builtin_fmaf(s[t / 2][t % 2 * 8 + e], c2, -ref));
+                    l += w[e];
                 }
+                const bf16x8_t p = __builtin_bit_cast(
+                    bf16x8_t, make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
+                                         pack_bf16x2(w[6], w[7])));
+                if (t < 3) {
+#pragma unroll
+                    for (int d = 0; d < L::kOut; ++d)
+                        vf[(t + 1) & 1][d] =
+                            read_columns((v_at ^ (d * 64)) + buf + 16 * (t + 1) * CH * 16, 8 * CH * 16);
+                }
+#pragma unroll
+                for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p, o[d]);
             }
         }
         if (i + 1 < n) write_tile(i + 1);

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kTokensPerBlock = 1024;   // tokens, and as many fresh or returned pages
+constexpr int kMaxBlocks = 512;
 constexpr int kFew = 2048;              // requests up to which the smaller LDS image serves
 
 // Exclusive prefix sums of three values per thread over the workgroup, and
@@ -174,10 +174,11 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(TablesArgs a) {
 }  // namespace
 
 hipError_t launch_kv_tables(const TablesArgs &a, hipStream_t st) {
-    int blocks = (a.T + kTokensPerBlock - 1) / kTokensPerBlock;
+    // A token per thread: its chain of lookups (request, lengths, page) is then walked once, all tokens' at a time.
+    int blocks = (a.T + kThreads - 1) / kThreads;
     const int by_requests = (a.num_requests + kThreads / 4 - 1) / (kThreads / 4);
     blocks = blocks > by_requests ? blocks : by_requests;
-    blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
+    blocks = blocks < 1 ? 1 : blocks > kMaxBlocks ? kMaxBlocks : blocks;
     if (a.num_requests <= kFew)
         hipLaunchKernelGGL((kv_tables_kernel<kFew>), dim3(blocks), dim3(kThreads), 0, st, a);
     else
