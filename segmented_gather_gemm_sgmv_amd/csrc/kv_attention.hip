@@ -409,28 +409,46 @@ __device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ bf16x8_t read_row(uint32_t at) {
-    return *(const __attribute__((address_space(3))) bf16x8_t *)(uintptr_t)at;
-}
-
-// Eight rows' values of one column per lane: rows of `at` and `step` past it.
-__device__ __forceinline__ bf16x8_t read_columns(uint32_t at, uint32_t step) {
+// Eight rows' values of one column per lane: four rows at `p`, four `step` bytes on.
+__device__ __forceinline__ bf16x8_t read_columns(const unsigned char *p, int step) {
     union {
         s16x4_t x[2];
         bf16x8_t v;
     } f;
-    f.x[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(uintptr_t)at);
-    f.x[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(uintptr_t)(at + step));
+    f.x[0] = read_transposed(p);
+    f.x[1] = read_transposed(p + step);
     return f.v;
 }
 
-template <int D>
+// 16 bytes per lane from base + off straight to LDS at `to` + 16 * lane (base and to uniform over the wave).
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t off, unsigned char *to, bool on) {
+    typedef const __attribute__((address_space(1))) char gchar_t;
+    typedef __attribute__((address_space(3))) unsigned char lchar_t;
+    if (on) __builtin_amdgcn_global_load_lds((gchar_t *)base + off, (lchar_t *)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Every wave's loads to LDS have landed, and its reads of LDS are done.
+__device__ __forceinline__ void loads_barrier() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+}
+
+// kFull: head_dim is D (no chunk of a row is past the head).
+template <int D, bool kFull>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
                                                            float *slots) {
     using L = Tile<D>;
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
-    __shared__ __align__(16) unsigned char lds[2][2][L::kBytes];  // buffer, K / V
+    // Two buffers of K and V. They are variables of their own, and the loop below names them statically, so that
+    // the compiler sees that a buffer's loads in flight have nothing to do with reads of the other one.
+    __shared__ __align__(16) unsigned char k_even[L::kBytes], v_even[L::kBytes], k_odd[L::kBytes], v_odd[L::kBytes];
     __shared__ PlanSmem plan;
     __shared__ int s_flag;
 
@@ -456,7 +474,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0;
     const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
-    const int nch = a.head_dim / 8;
+    const int head_dim = kFull ? D : a.head_dim, nch = head_dim / 8;
     bf16x8_t qf[CH / 2];
     {
         const bf16_t *q = static_cast<const bf16_t *>(a.q) + (int64_t)(it.q0 + (valid ? tok : 0)) * a.q_stride +
@@ -468,13 +486,14 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
             qf[k] = __builtin_bit_cast(bf16x8_t, valid && c < nch ? v : make_uint4(0, 0, 0, 0));
         }
     }
-    if (nch < CH) {  // a narrower head: the chunks past it stay zero
-        for (int i = tid; i < 4 * L::kBytes / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(lds)[i] = make_uint4(0, 0, 0, 0);
+    if (!kFull) {  // the chunks past the head stay zero: the chunks past it stay zero
+        for (int i = tid; i < L::kBytes / 16; i += kThreads)
+            for (unsigned char *buf : {k_even, v_even, k_odd, v_odd})
+                reinterpret_cast<uint4 *>(buf)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
 
-    const int row_bytes = a.head_dim * 2, page_mask = (1 << a.page_shift) - 1;
+    const int row_bytes = head_dim * 2, page_mask = (1 << a.page_shift) - 1;
     int pages = 0;  // of the next 16 tiles' 64 16-key blocks, one per lane
     auto load_pages = [&](int i) {
         const int v = t0 + i + lane / 4;
@@ -487,39 +506,24 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
             }
         }
     };
-    uint4 kr[NL], vr[NL];
-    auto load_tile = [&](int i) {
+    // Tile i goes straight to LDS: thread t fills 16-byte slots t, t + 256, ... of a buffer with the chunks that the
+    // swizzles put there. Rows of a 16-key block are one run of memory, so a thread's offset in it is the same for all.
+    constexpr int kBlockThreads = 16 * CH;  // threads that fill one 16-key block
+    const int slot_row = tid % kBlockThreads / CH, slot_chunk = tid % CH;
+    const int k_chunk = S::k_slot(slot_row, slot_chunk) - slot_row * CH, v_chunk = S::v_slot(slot_row, slot_chunk) - slot_row * CH;
+    const uint32_t k_off = slot_row * row_bytes + k_chunk * 16, v_off = slot_row * row_bytes + v_chunk * 16;
+    const int wave_u = __builtin_amdgcn_readfirstlane(wave);
+    auto load_tile = [&](int i, unsigned char *kb, unsigned char *vb) {
         const int key0 = run.tile(t0 + i) * kTileKeys;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int f = j * kThreads + tid, c = f % CH;
-            const int block = __builtin_amdgcn_readfirstlane(f / CH / 16);  // a wave's chunks lie in one block
+            const int block = j * (kThreads / kBlockThreads) + wave_u * 64 / kBlockThreads;
             const int page = __builtin_amdgcn_readlane(pages, i % 16 * 4 + block);
             const int64_t row =
                 (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + ((key0 + 16 * block) & page_mask);
-            const uint32_t off = (uint32_t)(f / CH % 16 * row_bytes + (c < nch ? c : 0) * 16);
-            kr[j] = ld16(static_cast<const char *>(a.K) + row * row_bytes + off);
-            vr[j] = ld16(static_cast<const char *>(a.V) + row * row_bytes + off);
-        }
-    };
-    auto write_tile = [&](int i) {
-        const int key0 = run.tile(t0 + i) * kTileKeys;
-        uint4 *kb = reinterpret_cast<uint4 *>(lds[i & 1][0]), *vb = reinterpret_cast<uint4 *>(lds[i & 1][1]);
-        if (!(key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
-            // Values of keys that no row sees meet zero weights, which a NaN would survive.
-#pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                const int key = key0 + (j * kThreads + tid) / CH;
-                if (key > pb || (key < pa_lo && key >= a.sinks)) vr[j] = make_uint4(0, 0, 0, 0);
-            }
-        }
-        if (tid % CH < nch) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                const int f = j * kThreads + tid, c = f % CH, row = f / CH;
-                kb[S::k_slot(row, c)] = kr[j];
-                vb[S::v_slot(row, c)] = vr[j];
-            }
+            const int at = (j * kThreads + wave_u * 64) * 16;
+            load_to_lds(static_cast<const char *>(a.K) + row * row_bytes, k_off, kb + at, k_chunk < nch);
+            load_to_lds(static_cast<const char *>(a.V) + row * row_bytes, v_off, vb + at, v_chunk < nch);
         }
     };
 
@@ -531,34 +535,40 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
 
-    // LDS addresses of this lane's fragments; the others of a tile differ from them by one exclusive or (the chunk)
-    // and a constant (the rows), which the swizzles leave alone.
-    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char *)&lds[0][0][0];
-    const uint32_t k_at = lds_at + S::k_slot(r, h) * 16;
-    const int v_row = 4 * h + ((lane & 15) >> 2);
-    const uint32_t v_at =
-        lds_at + L::kBytes + S::v_slot(v_row, 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) * 16 + 8 * (lane & 1);
+    // Offsets of this lane's fragments in a buffer's first rows: K rows r (32 of a product), chunk 2 k + h; V rows
+    // 4 h + 0..3, columns 32 d + 16 (lane / 16 % 2) + 0..15. Sixteen rows further on the swizzles are the same.
+    uint32_t k_at[CH / 2], v_at[L::kOut];
+#pragma unroll
+    for (int k = 0; k < CH / 2; ++k) k_at[k] = S::k_slot(r, 2 * k + h) * 16;
+#pragma unroll
+    for (int d = 0; d < L::kOut; ++d)
+        v_at[d] = S::v_slot(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) * 16 +
+                  8 * (lane & 1);
 
     const int n = t1 - t0;
-    if (n > 0) {
-        load_pages(0);
-        load_tile(0);
-        write_tile(0);
-    }
-    __syncthreads();
-    for (int i = 0; i < n; ++i) {
+    auto step = [&](int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
         if (i + 1 < n) {
             if ((i + 1) % 16 == 0) load_pages(i + 1);
-            load_tile(i + 1);
+            load_tile(i + 1, k_next, v_next);
         }
         const int key0 = run.tile(t0 + i) * kTileKeys;
-        const uint32_t buf = (i & 1) * 2 * L::kBytes;
-        const bool any = live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks);
-        if (any) {
-            // K fragments of the second 32 keys are read while the first 32's products run.
+        if (!(key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
+            // Values of keys that no row sees meet zero weights, which a NaN would survive.
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int f = j * kThreads + tid, key = key0 + f / CH;
+                if (key > pb || (key < pa_lo && key >= a.sinks))
+                    reinterpret_cast<uint4 *>(vb)[f] = make_uint4(0, 0, 0, 0);
+            }
+            lds_barrier();
+        }
+        if (live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks)) {
             bf16x8_t kf[2][CH / 2];
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) kf[0][k] = read_row((k_at ^ (k * 32)) + buf);
+            for (int k = 0; k < CH / 2; ++k) kf[0][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k]);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < CH / 2; ++k) kf[1][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k] + 32 * CH * 16);
             __builtin_amdgcn_sched_barrier(0);
             f32x16_t s[2];
 #pragma unroll
@@ -566,21 +576,12 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) {
-                kf[1][k] = read_row((k_at ^ (k * 32)) + buf + 32 * CH * 16);
-                s[0] = mfma32(kf[0][k], qf[k], s[0]);
-            }
-#pragma unroll
-            for (int k = 0; k < CH / 2; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read,
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int k = 0; k < CH / 2; ++k) s[0] = mfma32(kf[0][k], qf[k], s[0]);
 #pragma unroll
             for (int k = 0; k < CH / 2; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
             bf16x8_t vf[2][L::kOut];  // V fragments of two 16-key steps
 #pragma unroll
-            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns((v_at ^ (d * 64)) + buf, 8 * CH * 16);
+            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(vb + v_at[d], 8 * CH * 16);
             if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -620,15 +621,22 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
                 if (t < 3) {
 #pragma unroll
                     for (int d = 0; d < L::kOut; ++d)
-                        vf[(t + 1) & 1][d] =
-                            read_columns((v_at ^ (d * 64)) + buf + 16 * (t + 1) * CH * 16, 8 * CH * 16);
+                        vf[(t + 1) & 1][d] = read_columns(vb + v_at[d] + 16 * (t + 1) * CH * 16, 8 * CH * 16);
                 }
 #pragma unroll
                 for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p, o[d]);
             }
         }
-        if (i + 1 < n) write_tile(i + 1);
-        __syncthreads();
+        loads_barrier();
+    };
+    if (n > 0) {
+        load_pages(0);
+        load_tile(0, k_even, v_even);
+    }
+    loads_barrier();
+    for (int i = 0; i < n; i += 2) {
+        step(i, k_even, v_even, k_odd, v_odd);
+        if (i + 1 < n) step(i + 1, k_odd, v_odd, k_even, v_even);
     }
 
     l = swap32_sum(l);
@@ -644,7 +652,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
             for (int e = 0; e < 16; e += 4) {
                 const int at = 32 * d + 2 * e + 4 * h;
                 const f32x4_t x = {o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
-                if (at >= a.head_dim) continue;
+                if (at >= head_dim) continue;
                 if (splits == 1)
                     store_row4<bf16_t>(a, q_row, q_head, at, x, l);
                 else
@@ -664,7 +672,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     // The last of the group's items to arrive adds the splits up, in their order.
     uint32_t *counter = counters + it.first_slot;
     if (!arrive_last(counter, (uint32_t)splits, &s_flag)) return;
-    const int live = min(kTileRows, rows - row0), vecs = a.head_dim / 4;
+    const int live = min(kTileRows, rows - row0), vecs = head_dim / 4;
     for (int e = tid; e < live * vecs; e += kThreads) {
         const int row = e / vecs, d = e % vecs * 4;
         float top = kNone;
@@ -736,8 +744,11 @@ hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
     const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
     const int64_t groups = most_groups(a, longs, kTileRows);
     const int take = one ? kTakeAll : kTakeLong;
-    const hipError_t e = a.head_dim <= 64 ? launch(tile_kernel<64>, a, take, groups, kTileTarget, st)
-                                          : launch(tile_kernel<128>, a, take, groups, kTileTarget, st);
+    const auto kernel = a.head_dim == 64    ? tile_kernel<64, true>
+                        : a.head_dim == 128 ? tile_kernel<128, true>
+                        : a.head_dim < 64   ? tile_kernel<64, false>
+                                            : tile_kernel<128, false>;
+    const hipError_t e = launch(kernel, a, take, groups, kTileTarget, st);
     if (e != hipSuccess || one) return e;
     return launch_stream<bf16_t>(a, kTakeShort, a.num_requests, st);
 }
