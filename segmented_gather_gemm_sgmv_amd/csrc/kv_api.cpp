@@ -144,6 +144,9 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
         max_blocks < 0 || window < 0 || sinks < 0)
         return SGMV_ERR_SHAPE;
     if ((int64_t)T * q_heads > INT32_MAX || (int64_t)max_q_len * q_heads > INT32_MAX) return SGMV_ERR_SHAPE;
+    // the kernels number their items, at most these, in 31 bits
+    const int64_t rows = (int64_t)(max_q_len < T ? max_q_len : T) * (q_heads / kv_heads);
+    if (((rows / 16 + 1) * kv_heads + sgmv::kMostSplits) * num_requests > INT32_MAX) return SGMV_ERR_SHAPE;
     int st = check_pages(num_pages, page_size);
     if (st != SGMV_OK) return st;
     if ((int64_t)max_blocks * page_size > INT32_MAX) return SGMV_ERR_SHAPE;

@@ -6,11 +6,12 @@
 // themselves. The rows of a request's tokens for one cached head are packed
 // (token, then query head of the group) and cut into row tiles; a (request,
 // row tile, cached head) is a group. The key tiles of a long group are split
-// into runs of `chunk` tiles, so that the whole batch makes about as many
-// items as the GPU runs at once; chunk depends on the batch's total work
+// into runs of about `chunk` tiles, so that the whole batch makes about as
+// many items as the GPU runs at once; chunk depends on the batch's total work
 // alone, so a few long requests among many short ones still spread over the
-// chip. Every workgroup forms the same sums over all requests (8 bytes per
-// request, from L2) and picks the item of its own index.
+// chip. Every wave forms the same sums over all requests (8 bytes per request,
+// from L2; a scan over the wave's lanes, no LDS and no barrier) and picks the
+// item of its workgroup's index.
 #pragma once
 
 #include "kv_launch.h"
@@ -80,95 +81,111 @@ __device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int s
 struct Item {
     int b, q0, n, p0;
     int row_tile, head;
-    int split, chunk;  // this item's run of virtual tiles: [split * chunk, ...)
-    int first_slot;    // partial-result slot of the group's split 0 of this request's first group
-    int splits;        // splits every group of the request is given
+    int split, size;   // this item's run of virtual tiles: [split * size, (split + 1) * size)
+    int first_slot;    // partial-result slot of the group's split 0
 };
 
-struct PlanSmem {
-    unsigned long long wave[kWaves];
-    Item item;
-    int found;
-};
+template <int kCtrl, int kRowMask, typename V>
+__device__ __forceinline__ V shifted(V v) {
+    return __builtin_bit_cast(
+        V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), kCtrl, kRowMask, 0xf, false));
+}
 
-__device__ __forceinline__ unsigned long long wave_sum(unsigned long long v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+// Inclusive prefix sum over the wave's lanes.
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v) {
+    v += shifted<0x111, 0xf>(v);  // the lane 1, 2, 4, 8 below, within rows of 16 lanes
+    v += shifted<0x112, 0xf>(v);
+    v += shifted<0x114, 0xf>(v);
+    v += shifted<0x118, 0xf>(v);
+    v += shifted<0x142, 0xa>(v);  // row 0's last lane to row 1, row 2's to row 3
+    v += shifted<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
     return v;
 }
 
-// The item of this workgroup. Returns false if it has none (the grid is an
-// upper bound), or if the sums do not fit the launch (only metadata outside
-// the documented ranges does that): every workgroup then sees the same and
-// none does anything.
+// The item of workgroup `index` of a grid of `grid`, found by every wave for
+// itself: lane i looks at requests i * per ... Returns false if there is none
+// (the grid is an upper bound), or if the items do not fit the grid (only
+// metadata outside the documented ranges does that): every workgroup then
+// sees the same and none does anything. kBatch: requests per lane whose
+// lengths are read at once.
+template <int kRows, int kKeys, int kBatch>
+__device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
+                                             int index, int grid, Item &it) {
+    const int lane = threadIdx.x & 63, B = a.num_requests;
+    const int per = kBatch == 1 ? 1 : (B + 63) / 64, first = lane * per;
+    Share s[kBatch];
+    const auto read = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int b = first + j0 + j;
+            s[j] = j0 + j < per && b < B ? share<kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
+        }
+    };
+    // The batch's work in key tiles; its rounding is the same for every wave.
+    float work = 0.f;
+    for (int j0 = 0; j0 < per; j0 += kBatch) {
+        read(j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) work += (float)s[j].row_tiles * (float)max(s[j].tiles, 1);
+    }
+    work = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wave_scan(work)), 63));
+    const int chunk = max((int)fminf(ceilf(work * a.kv_heads / target), 1e9f), min_chunk);
+
+    // A group is split where it is at least one and a half chunks long; the
+    // groups that are split then have at most 4/3 * target parts together.
+    const auto splits_of = [&](const Share &x) { return max((x.tiles + chunk / 2) / chunk, 1); };
+    int items = 0, slots = 0;
+    for (int j0 = 0; j0 < per; j0 += kBatch) {
+        if (per > kBatch) read(j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int splits = splits_of(s[j]), parts = s[j].row_tiles * a.kv_heads * splits;
+            items += parts;
+            slots += splits > 1 ? parts : 0;
+        }
+    }
+    const int items_to = wave_scan(items), slots_to = wave_scan(slots);
+    if (__builtin_amdgcn_readlane(items_to, 63) > grid) return false;
+    int at = index - (items_to - items), slot = slots_to - slots;
+    bool mine = at >= 0 && at < items;
+    const unsigned long long who = __ballot(mine);
+    if (who == 0) return false;
+    Share x = s[0];
+    int b = first;
+    if (kBatch > 1 && mine) {
+        for (int j = 0; j < per; ++j) {
+            x = share<kRows, kKeys>(a, first + j, take, short_rows);
+            const int splits = splits_of(x), parts = x.row_tiles * a.kv_heads * splits;
+            b = first + j;
+            if (at < parts) break;
+            at -= parts;
+            slot += splits > 1 ? parts : 0;
+        }
+    }
+    const int splits = splits_of(x), j = at / a.kv_heads, head = at % a.kv_heads;
+    const int row_tile = x.row_tiles - 1 - j / splits;  // the tiles that see the most keys first
+    const int size = (x.tiles + splits - 1) / splits;
+    const int src = __ffsll((unsigned long long)who) - 1;
+    const auto get = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+    it.b = get(b);
+    it.q0 = get(x.q0);
+    it.n = get(x.n);
+    it.p0 = get(x.p0);
+    it.row_tile = get(row_tile);
+    it.head = get(head);
+    it.split = get(j % splits);
+    it.size = get(size);
+    it.first_slot = get(slot + (head * x.row_tiles + row_tile) * splits);
+    return true;
+}
+
 template <int kRows, int kKeys>
 __device__ __forceinline__ bool find_item(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
-                                          int index, int grid, PlanSmem &sm, Item &out) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, B = a.num_requests;
-    const unsigned long long heads = a.kv_heads;
-    Share first = {0, 0, 0, 0, 0};
-    unsigned long long work = 0;
-    for (int b = tid; b < B; b += kThreads) {
-        const Share s = share<kRows, kKeys>(a, b, take, short_rows);
-        if (b == tid) first = s;
-        work += (unsigned long long)s.row_tiles * max(s.tiles, 1) * heads;
-    }
-    work = wave_sum(work);
-    if (lane == 0) sm.wave[wave] = work;
-    if (tid == 0) sm.found = 0;
-    __syncthreads();
-    work = sm.wave[0] + sm.wave[1] + sm.wave[2] + sm.wave[3];
-    const unsigned long long per = (work + target - 1) / target;
-    const int chunk = per > (unsigned)min_chunk ? (int)min(per, 0x40000000ull) : min_chunk;
-
-    // Items in the low 40 bits, partial-result slots above: a request gives
-    // at most 2^20 items here, and all of them at most 2 * target slots,
-    // since a group of t tiles is split only if t > chunk >= work / target.
-    unsigned long long base = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        const int b = b0 + tid;
-        Share s = first;
-        if (b0 > 0) s = b < B ? share<kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
-        const int splits = max((s.tiles + chunk - 1) / chunk, 1);
-        const unsigned long long groups = (unsigned long long)s.row_tiles * heads;
-        const unsigned long long items = min(groups * splits, 1ull << 20);
-        const unsigned long long mine = items | (splits > 1 ? groups * splits : 0) << 40;
-        unsigned long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const unsigned long long up = __shfl_up(incl, o);
-            if (lane >= o) incl += up;
-        }
-        __syncthreads();
-        if (lane == 63) sm.wave[wave] = incl;
-        __syncthreads();
-        unsigned long long before = base;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += sm.wave[w];
-            base += sm.wave[w];
-        }
-        before += incl - mine;
-        const long long at = (long long)index - (long long)(before & ((1ull << 40) - 1));
-        if (at >= 0 && at < (long long)items) {
-            const int j = (int)at / a.kv_heads;
-            Item &it = sm.item;
-            it.b = b;
-            it.q0 = s.q0;
-            it.n = s.n;
-            it.p0 = s.p0;
-            it.head = (int)at % a.kv_heads;
-            it.row_tile = s.row_tiles - 1 - j / splits;  // the tiles that see the most keys first
-            it.split = j % splits;
-            it.chunk = chunk;
-            it.splits = splits;
-            it.first_slot = (int)(before >> 40) + (it.head * s.row_tiles + it.row_tile) * splits;
-            sm.found = 1;
-        }
-    }
-    __syncthreads();
-    out = sm.item;
-    return sm.found && (base & ((1ull << 40) - 1)) <= (unsigned long long)grid;
+                                          int index, int grid, Item &it) {
+    return a.num_requests <= 64
+               ? find_item_of<kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, index, grid, it)
+               : find_item_of<kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, index, grid, it);
 }
 
 // Maximum and sum over the four lanes (l, l ^ 16, l ^ 32, l ^ 48) that hold

@@ -119,22 +119,21 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
     using S = Stream<T, D>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     __shared__ __align__(16) unsigned char lds[S::kLdsBytes];
-    __shared__ PlanSmem plan;
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
     __shared__ int s_flag;
 
     Item it;
     if (!find_item<kStreamRows, S::kKeys>(a, take, short_rows, kStreamTarget, kStreamMinChunk, blockIdx.x, gridDim.x,
-                                          plan, it))
+                                          it))
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
     const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
     const int pa = it.p0 + tok_a, pb = it.p0 + tok_b;
     const TileRun run = tile_run<S::kKeys>(pa, pb, a.window, a.sinks);
-    const int splits = max((run.count + it.chunk - 1) / it.chunk, 1);
+    const int splits = run.count > it.size ? (run.count + it.size - 1) / it.size : 1;
     if (it.split >= splits) return;
-    const int t1 = min(run.count, (it.split + 1) * it.chunk);
+    const int t1 = min(run.count, (it.split + 1) * it.size);
 
     // This lane's row: query fragments, position, first key of its window.
     const int my = row0 + r, tok = my / a.group;
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
     const int row_bytes = a.head_dim * (int)sizeof(T);
     const int page_mask = (1 << a.page_shift) - 1;
     int pages = 0;
-    const int first = it.split * it.chunk + wave;
+    const int first = it.split * it.size + wave;
     auto load_pages = [&](int i) {  // the wave's tiles i, i + 1, ...
         const int v = first + kWaves * (i + lane / NB);
         pages = 0;
@@ -449,20 +448,19 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     // Two buffers of K and V. They are variables of their own, and the loop below names them statically, so that
     // the compiler sees that a buffer's loads in flight have nothing to do with reads of the other one.
     __shared__ __align__(16) unsigned char k_even[L::kBytes], v_even[L::kBytes], k_odd[L::kBytes], v_odd[L::kBytes];
-    __shared__ PlanSmem plan;
     __shared__ int s_flag;
 
     Item it;
-    if (!find_item<kTileRows, kTileKeys>(a, take, short_rows, kTileTarget, kTileMinChunk, blockIdx.x, gridDim.x, plan,
+    if (!find_item<kTileRows, kTileKeys>(a, take, short_rows, kTileTarget, kTileMinChunk, blockIdx.x, gridDim.x,
                                          it))
         return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
     const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
     const TileRun run = tile_run<kTileKeys>(pa, pb, a.window, a.sinks);
-    const int splits = max((run.count + it.chunk - 1) / it.chunk, 1);
+    const int splits = run.count > it.size ? (run.count + it.size - 1) / it.size : 1;
     if (it.split >= splits) return;
-    const int t0 = it.split * it.chunk, t1 = min(run.count, t0 + it.chunk);
+    const int t0 = it.split * it.size, t1 = min(run.count, t0 + it.size);
 
     const int wrow = row0 + 32 * wave;  // this wave's rows; past the last row it only helps loading
     const bool live_wave = wrow < rows;
@@ -698,8 +696,9 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
 // ----------------------------------------------------------------------------
 // Launches and workspace
 // ----------------------------------------------------------------------------
-constexpr int kMaxSlots = 2 * (kStreamTarget > kTileTarget ? kStreamTarget : kTileTarget);
-constexpr size_t kCounterBytes = (size_t)kMaxSlots * sizeof(uint32_t);
+// The groups that a launch splits have at most 4/3 * its target parts.
+constexpr size_t kCounterBytes = (size_t)kMostSplits * sizeof(uint32_t);
+static_assert(4 * kStreamTarget <= 3 * kMostSplits && 4 * kTileTarget <= 3 * kMostSplits, "slots for every split");
 
 // The most groups of `rows` packed rows that requests of up to max_q_len
 // tokens, T in all, can make: every request's last group may be part full.
@@ -729,8 +728,8 @@ hipError_t launch_stream(const AttnArgs &a, int take, int64_t groups, hipStream_
 
 size_t attention_workspace_bytes(int head_dim, int dtype) {
     const size_t d = head_dim <= 64 ? 64 : 128;
-    const size_t stream = 2 * kStreamTarget * (kStreamRows * d + 2 * kStreamRows);
-    const size_t tile = dtype == SGMV_BF16 ? 2 * kTileTarget * (kTileRows * d + 2 * kTileRows) : 0;
+    const size_t stream = (size_t)kMostSplits * (kStreamRows * d + 2 * kStreamRows);
+    const size_t tile = dtype == SGMV_BF16 ? (size_t)kMostSplits * (kTileRows * d + 2 * kTileRows) : 0;
     return kCounterBytes + (stream > tile ? stream : tile) * sizeof(float);
 }
 

@@ -65,6 +65,9 @@ struct AttnArgs {
     void *workspace;
 };
 
+// Partial-result slots of a launch: no launch splits its groups into more parts.
+constexpr int kMostSplits = 1024;
+
 // Workspace of sgmv_paged_attention: counters first, then the partial-result
 // slots of the launch that splits the most.
 size_t attention_workspace_bytes(int head_dim, int dtype);
