@@ -39,6 +39,13 @@ constexpr int kStreamRows = 16;
 constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
 constexpr int kStreamMinChunk = 16;  // key tiles a split has at least (four per wave)
 
+constexpr int kShortRows = 16;       // bf16 groups up to this many rows; longer ones go to the tile kernel
+
+struct StreamSmem {
+    float m[kWaves][16], l[kWaves][16];  // the waves' running maxima and sums
+    int flag;
+};
+
 template <typename T, int D>
 struct Stream {
     static constexpr bool kBf16 = Elem<T>::kPerVec == 8;
@@ -49,9 +56,8 @@ struct Stream {
     static constexpr int kTileBytes = kKeys * kChunks * 16;
     static constexpr int kOut = D / 16;               // 16-column blocks of the output
     static constexpr int kOutStride = D + 4;          // floats per row of the waves' results in LDS
-    static constexpr int kLdsBytes = kWaves * 2 * kTileBytes > kWaves * 16 * kOutStride * 4
-                                         ? kWaves * 2 * kTileBytes
-                                         : kWaves * 16 * kOutStride * 4;
+    static constexpr int kOutBytes = 16 * kOutStride * 4;
+    static constexpr int kWaveBytes = 2 * kTileBytes > kOutBytes ? 2 * kTileBytes : kOutBytes;  // one wave's LDS
     static constexpr int kSlotFloats = 16 * D + 32;   // partial result: 16 x D sums, 16 maxima, 16 weight sums
 
     // Chunk c of row r sits in chunk slot c ^ swizzle(r): the 16 rows that one
@@ -113,19 +119,15 @@ __device__ __forceinline__ float lse_of(float m, float weight) {
     return weight > 0.f || weight != weight ? m * kLn2 + logf(weight) : kNone;
 }
 
+// Item `index` of `grid`. The four LDS regions (kWaveBytes each) are the four waves' own.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
-                                                             float *slots) {
+__device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
+                                            float *slots, unsigned char *lds0, unsigned char *lds1,
+                                            unsigned char *lds2, unsigned char *lds3, StreamSmem &sm) {
     using S = Stream<T, D>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
-    __shared__ __align__(16) unsigned char lds[S::kLdsBytes];
-    __shared__ float s_m[kWaves][16], s_l[kWaves][16];
-    __shared__ int s_flag;
-
     Item it;
-    if (!find_item<kStreamRows, S::kKeys>(a, take, short_rows, kStreamTarget, kStreamMinChunk, blockIdx.x, gridDim.x,
-                                          it))
-        return;
+    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
     const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
@@ -155,7 +157,8 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
         }
     }
 
-    unsigned char *k_lds = lds + wave * 2 * S::kTileBytes, *v_lds = k_lds + S::kTileBytes;
+    const auto region = [&](int w) { return w == 0 ? lds0 : w == 1 ? lds1 : w == 2 ? lds2 : lds3; };
+    unsigned char *k_lds = region(wave), *v_lds = k_lds + S::kTileBytes;
     if (nch < CH) {  // a narrower head: the chunks past it stay zero
         for (int i = lane; i < 2 * S::kTileBytes / 16; i += 64)
             reinterpret_cast<uint4 *>(k_lds)[i] = make_uint4(0, 0, 0, 0);
@@ -311,13 +314,13 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
     // The four waves' results meet in LDS, in wave order.
     l = swap32_sum(swap16_sum(l));
     if (g == 0) {
-        s_m[wave][r] = m;
-        s_l[wave][r] = l;
+        sm.m[wave][r] = m;
+        sm.l[wave][r] = l;
     }
     __syncthreads();
-    const float m_all = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+    const float m_all = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
     const float keep = exp2_fast(m - ref_of(m_all));
-    float *o_lds = reinterpret_cast<float *>(lds) + (wave * 16 + r) * S::kOutStride;
+    float *o_lds = reinterpret_cast<float *>(k_lds) + r * S::kOutStride;
 #pragma unroll
     for (int d = 0; d < S::kOut; ++d) *reinterpret_cast<f32x4_t *>(o_lds + 16 * d + 4 * g) = o[d] * keep;
     __syncthreads();
@@ -331,12 +334,11 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
         f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
         float top = kNone, weight = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w][row]);
+        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sm.m[w][row]);
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            sum += *reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(lds) +
-                                                      (w * 16 + row) * S::kOutStride + d);
-            weight += s_l[w][row] * exp2_fast(s_m[w][row] - ref_of(top));
+            sum += *reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(region(w)) + row * S::kOutStride + d);
+            weight += sm.l[w][row] * exp2_fast(sm.m[w][row] - ref_of(top));
         }
         if (splits == 1) {
             const int at = row0 + row, head = it.head * a.group + at % a.group;
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, int tak
 
     // The last of the group's items to arrive adds the splits up, in their order.
     uint32_t *counter = counters + it.first_slot;
-    if (!arrive_last(counter, (uint32_t)splits, &s_flag)) return;
+    if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
     for (int e = tid; e < live * vecs; e += kThreads) {
         const int row = e / vecs, d = e % vecs * 4;
         float top = kNone;
@@ -393,7 +395,6 @@ constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr int kTileTarget = 512;   // as kStreamTarget
 constexpr int kTileMinChunk = 8;   // key tiles a split has at least
-constexpr int kShortRows = 16;     // groups up to this many rows go to the streaming kernel
 
 template <int D>
 struct Tile {
@@ -440,20 +441,14 @@ __device__ __forceinline__ void loads_barrier() {
 
 // kFull: head_dim is D (no chunk of a row is past the head).
 template <int D, bool kFull>
-__global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take, int short_rows, uint32_t *counters,
-                                                           float *slots) {
+__device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
+                                          float *slots, unsigned char *k_even, unsigned char *v_even,
+                                          unsigned char *k_odd, unsigned char *v_odd, int *s_flag) {
     using L = Tile<D>;
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
-    // Two buffers of K and V. They are variables of their own, and the loop below names them statically, so that
-    // the compiler sees that a buffer's loads in flight have nothing to do with reads of the other one.
-    __shared__ __align__(16) unsigned char k_even[L::kBytes], v_even[L::kBytes], k_odd[L::kBytes], v_odd[L::kBytes];
-    __shared__ int s_flag;
-
     Item it;
-    if (!find_item<kTileRows, kTileKeys>(a, take, short_rows, kTileTarget, kTileMinChunk, blockIdx.x, gridDim.x,
-                                         it))
-        return;
+    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
     const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
@@ -669,7 +664,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
 
     // The last of the group's items to arrive adds the splits up, in their order.
     uint32_t *counter = counters + it.first_slot;
-    if (!arrive_last(counter, (uint32_t)splits, &s_flag)) return;
+    if (!arrive_last(counter, (uint32_t)splits, s_flag)) return;
     const int live = min(kTileRows, rows - row0), vecs = head_dim / 4;
     for (int e = tid; e < live * vecs; e += kThreads) {
         const int row = e / vecs, d = e % vecs * 4;
@@ -693,11 +688,38 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int take,
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, uint32_t *counters, float *slots) {
+    using S = Stream<T, D>;
+    __shared__ __align__(16) unsigned char lds[kWaves][S::kWaveBytes];
+    __shared__ StreamSmem sm;
+    stream_item<T, D>(a, kTakeAll, blockIdx.x, gridDim.x, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
+}
+
+// Workgroups below `tiles` take the tile items, the others the streaming
+// items, each with counters and slots of its own: in a batch of both, the
+// ones compute while the others read.
+template <int D, bool kFull>
+__global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles, uint32_t *counters, float *slots) {
+    // Two buffers of K and V. They are variables of their own, and the loop names them statically, so that the
+    // compiler sees that a buffer's loads in flight have nothing to do with reads of the other one.
+    constexpr int kBytes = Tile<D>::kBytes > Stream<bf16_t, D>::kWaveBytes ? Tile<D>::kBytes : Stream<bf16_t, D>::kWaveBytes;
+    __shared__ __align__(16) unsigned char k_even[kBytes], v_even[kBytes], k_odd[kBytes], v_odd[kBytes];
+    __shared__ StreamSmem sm;
+    const int index = blockIdx.x;
+    if (index < tiles)
+        tile_item<D, kFull>(a, gridDim.x == (unsigned)tiles ? kTakeAll : kTakeLong, index, tiles, counters, slots,
+                            k_even, v_even, k_odd, v_odd, &sm.flag);
+    else
+        stream_item<bf16_t, D>(a, kTakeShort, index - tiles, gridDim.x - tiles, counters + kMostSplits,
+                               slots + (int64_t)kMostSplits * Tile<D>::kSlotFloats, k_even, v_even, k_odd, v_odd, sm);
+}
+
 // ----------------------------------------------------------------------------
 // Launches and workspace
 // ----------------------------------------------------------------------------
 // The groups that a launch splits have at most 4/3 * its target parts.
-constexpr size_t kCounterBytes = (size_t)kMostSplits * sizeof(uint32_t);
+constexpr size_t kCounterBytes = (size_t)2 * kMostSplits * sizeof(uint32_t);
 static_assert(4 * kStreamTarget <= 3 * kMostSplits && 4 * kTileTarget <= 3 * kMostSplits, "slots for every split");
 
 // The most groups of `rows` packed rows that requests of up to max_q_len
@@ -708,48 +730,46 @@ int64_t most_groups(const AttnArgs &a, int64_t requests, int rows) {
     return per * requests < by_rows ? per * requests : by_rows;
 }
 
-template <typename Kernel>
-hipError_t launch(Kernel kernel, const AttnArgs &a, int take, int64_t groups, int target, hipStream_t st) {
-    const int64_t grid = groups * a.kv_heads + target;
-    if (grid > (int64_t)1 << 24) return hipErrorInvalidValue;
-    char *ws = static_cast<char *>(a.workspace);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, a, take, kShortRows,
-                       reinterpret_cast<uint32_t *>(ws), reinterpret_cast<float *>(ws + kCounterBytes));
-    return hipGetLastError();
-}
+uint32_t *counters_of(const AttnArgs &a) { return static_cast<uint32_t *>(a.workspace); }
+float *slots_of(const AttnArgs &a) { return reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes); }
 
 template <typename T>
-hipError_t launch_stream(const AttnArgs &a, int take, int64_t groups, hipStream_t st) {
-    return a.head_dim <= 64 ? launch(stream_kernel<T, 64>, a, take, groups, kStreamTarget, st)
-                            : launch(stream_kernel<T, 128>, a, take, groups, kStreamTarget, st);
+hipError_t launch_stream(const AttnArgs &a, int64_t groups, hipStream_t st) {
+    const int64_t grid = groups * a.kv_heads + kStreamTarget;
+    if (grid > (int64_t)1 << 24) return hipErrorInvalidValue;
+    const auto kernel = a.head_dim <= 64 ? stream_kernel<T, 64> : stream_kernel<T, 128>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, a, counters_of(a), slots_of(a));
+    return hipGetLastError();
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int head_dim, int dtype) {
     const size_t d = head_dim <= 64 ? 64 : 128;
-    const size_t stream = (size_t)kMostSplits * (kStreamRows * d + 2 * kStreamRows);
-    const size_t tile = dtype == SGMV_BF16 ? (size_t)kMostSplits * (kTileRows * d + 2 * kTileRows) : 0;
-    return kCounterBytes + (stream > tile ? stream : tile) * sizeof(float);
+    const size_t stream = kStreamRows * d + 2 * kStreamRows;
+    const size_t tile = dtype == SGMV_BF16 ? kTileRows * d + 2 * kTileRows : 0;
+    return kCounterBytes + (size_t)kMostSplits * (stream + tile) * sizeof(float);
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-    if (a.dtype != SGMV_BF16) return launch_stream<float>(a, kTakeAll, most_groups(a, a.num_requests, kStreamRows), st);
+    if (a.dtype != SGMV_BF16) return launch_stream<float>(a, most_groups(a, a.num_requests, kStreamRows), st);
     // A batch whose requests all fit one row tile of the streaming kernel is its alone.
-    if ((int64_t)a.max_q_len * a.group <= kShortRows) return launch_stream<bf16_t>(a, kTakeAll, a.num_requests, st);
-    // Otherwise requests go to the two kernels by their rows. At most T * group / (kShortRows + 1) of them are long.
+    if ((int64_t)a.max_q_len * a.group <= kShortRows) return launch_stream<bf16_t>(a, a.num_requests, st);
+    // Otherwise requests go to the two kinds of items by their rows. At most T * group / (kShortRows + 1) are long; a
+    // batch of one request has tile items only.
     const int64_t could = (int64_t)a.T * a.group / (kShortRows + 1);
     const bool one = a.num_requests == 1;
     const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
-    const int64_t groups = most_groups(a, longs, kTileRows);
-    const int take = one ? kTakeAll : kTakeLong;
+    const int64_t tiles = most_groups(a, longs, kTileRows) * a.kv_heads + kTileTarget;
+    const int64_t streams = one ? 0 : (int64_t)a.num_requests * a.kv_heads + kStreamTarget;
+    if (tiles + streams > (int64_t)1 << 24) return hipErrorInvalidValue;
     const auto kernel = a.head_dim == 64    ? tile_kernel<64, true>
                         : a.head_dim == 128 ? tile_kernel<128, true>
                         : a.head_dim < 64   ? tile_kernel<64, false>
                                             : tile_kernel<128, false>;
-    const hipError_t e = launch(kernel, a, take, groups, kTileTarget, st);
-    if (e != hipSuccess || one) return e;
-    return launch_stream<bf16_t>(a, kTakeShort, a.num_requests, st);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles + streams)), dim3(kThreads), 0, st, a, (int)tiles, counters_of(a),
+                       slots_of(a));
+    return hipGetLastError();
 }
 
 }  // namespace sgmv
