@@ -37,12 +37,14 @@ constexpr float kSlack = 8.f;
 // ----------------------------------------------------------------------------
 constexpr int kStreamRows = 16;
 constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
-constexpr int kStreamMinChunk = 16;  // key tiles a split has at least (four per wave)
+constexpr int kStreamMinChunk = 16;  // key tiles a split has about at least (four per wave)
+constexpr int kStreamMaxSplits = 256;  // of one group
 
 constexpr int kShortRows = 16;       // bf16 groups up to this many rows; longer ones go to the tile kernel
 
 struct StreamSmem {
     float m[kWaves][16], l[kWaves][16];  // the waves' running maxima and sums
+    float part[2][kThreads];             // add_splits
     int flag;
 };
 
@@ -119,6 +121,84 @@ __device__ __forceinline__ float lse_of(float m, float weight) {
     return weight > 0.f || weight != weight ? m * kLn2 + logf(weight) : kNone;
 }
 
+// The last of a group's items to arrive adds the splits up, in their order.
+// Slots hold kRows x D sums, then the rows' maxima, then their weight sums.
+// All of the maxima are read first, each thread's in one go, and the splits'
+// factors left in LDS; then the sums, kAtOnce 4-column pieces and four splits
+// at a time: what this costs is the latency of reads from other XCDs, so as
+// many as possible are in flight.
+template <typename T, int D, int kRows, int kMaxSplits, int kAtOnce, typename Region>
+__device__ __forceinline__ void add_splits(const AttnArgs &a, const Item &it, int splits, int row0, int live,
+                                           __amdgpu_buffer_rsrc_t part, const Region &region, StreamSmem &sm) {
+    constexpr int kSlot = kRows * D + 2 * kRows, kParts = kThreads / kRows, kEach = kMaxSplits / kParts;
+    const int tid = threadIdx.x;
+    const auto factor = [&](int row) {  // splits' factors of a row, kMaxSplits apart
+        return reinterpret_cast<float *>(region(row / (kRows / kWaves))) + row % (kRows / kWaves) * kMaxSplits;
+    };
+    {
+        const int row = tid % kRows, p = tid / kRows;
+        float m[kEach], l[kEach], top = kNone, weight = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = min(p + i * kParts, splits - 1);  // a split read twice is not counted twice below
+            m[i] = part_load1(part, ((uint32_t)k * kSlot + kRows * D + row) * 4);
+            l[i] = part_load1(part, ((uint32_t)k * kSlot + kRows * D + kRows + row) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) top = fmaxf(top, m[i]);
+        sm.part[0][tid] = top;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) top = fmaxf(top, sm.part[0][q * kRows + row]);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int k = p + i * kParts;
+            if (k < splits) {
+                const float f = exp2_fast(m[i] - ref_of(top));
+                factor(row)[k] = f;
+                weight += f * l[i];
+            }
+        }
+        sm.part[1][tid] = weight;
+        __syncthreads();
+        if (p == 0) {
+            weight = 0.f;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) weight += sm.part[1][q * kRows + row];
+            sm.part[0][row] = weight;  // only the threads p == 0 of this row read part[0][row] after the barrier above
+            if (a.lse && row < live) {
+                const int at = row0 + row;
+                a.lse[(int64_t)(it.q0 + at / a.group) * a.q_heads + it.head * a.group + at % a.group] = lse_of(top, weight);
+            }
+        }
+        __syncthreads();
+    }
+    const int vecs = a.head_dim / 4, pieces = live * vecs;
+    for (int e0 = tid; e0 < pieces; e0 += kThreads * kAtOnce) {
+        f32x4_t sum[kAtOnce];
+        const float *f[kAtOnce];
+        uint32_t at[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int e = min(e0 + u * kThreads, pieces - 1);
+            sum[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            f[u] = factor(e / vecs);
+            at[u] = (e / vecs * D + e % vecs * 4) * 4;
+        }
+#pragma unroll 16 / kAtOnce
+        for (int k = 0; k < splits; ++k)
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) sum[u] += part_load(part, (uint32_t)k * kSlot * 4 + at[u]) * f[u][k];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int e = e0 + u * kThreads;
+            if (e >= pieces) break;
+            const int row = e / vecs, to = row0 + row;
+            store_row4<T>(a, it.q0 + to / a.group, it.head * a.group + to % a.group, e % vecs * 4, sum[u], sm.part[0][row]);
+        }
+    }
+}
+
 // Item `index` of `grid`. The four LDS regions (kWaveBytes each) are the four waves' own.
 template <typename T, int D>
 __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
@@ -127,7 +207,8 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     using S = Stream<T, D>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     Item it;
-    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, index, grid, it)) return;
+    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMaxSplits, index,
+                                              grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
     const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
@@ -356,28 +437,9 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     }
     if (splits == 1) return;
 
-    // The last of the group's items to arrive adds the splits up, in their order.
     uint32_t *counter = counters + it.first_slot;
     if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
-    for (int e = tid; e < live * vecs; e += kThreads) {
-        const int row = e / vecs, d = e % vecs * 4;
-        float top = kNone;
-        for (int k = 0; k < splits; ++k)
-            top = fmaxf(top, part_load1(part, ((uint32_t)k * S::kSlotFloats + 16 * D + row) * 4));
-        const float ref = ref_of(top);
-        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        float weight = 0.f;
-        for (int k = 0; k < splits; ++k) {
-            const uint32_t slot = (uint32_t)k * S::kSlotFloats;
-            const float keep_k = exp2_fast(part_load1(part, (slot + 16 * D + row) * 4) - ref);
-            weight += keep_k * part_load1(part, (slot + 16 * D + 16 + row) * 4);
-            sum += part_load(part, (slot + row * D + d) * 4) * keep_k;
-        }
-        const int at = row0 + row, head = it.head * a.group + at % a.group;
-        const int64_t q_row = it.q0 + at / a.group;
-        store_row4<T>(a, q_row, head, d, sum, weight);
-        if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
-    }
+    add_splits<T, D, kStreamRows, kStreamMaxSplits, 1>(a, it, splits, row0, live, part, region, sm);
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
@@ -394,7 +456,8 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr int kTileTarget = 512;   // as kStreamTarget
-constexpr int kTileMinChunk = 8;   // key tiles a split has at least
+constexpr int kTileMinChunk = 8;   // key tiles a split has about at least
+constexpr int kTileMaxSplits = 64; // of one group
 
 template <int D>
 struct Tile {
@@ -443,12 +506,12 @@ __device__ __forceinline__ void loads_barrier() {
 template <int D, bool kFull>
 __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
                                           float *slots, unsigned char *k_even, unsigned char *v_even,
-                                          unsigned char *k_odd, unsigned char *v_odd, int *s_flag) {
+                                          unsigned char *k_odd, unsigned char *v_odd, StreamSmem &sm) {
     using L = Tile<D>;
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
-    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, index, grid, it)) return;
+    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMaxSplits, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
     const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
@@ -662,34 +725,15 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     }
     if (splits == 1) return;
 
-    // The last of the group's items to arrive adds the splits up, in their order.
     uint32_t *counter = counters + it.first_slot;
-    if (!arrive_last(counter, (uint32_t)splits, s_flag)) return;
-    const int live = min(kTileRows, rows - row0), vecs = head_dim / 4;
-    for (int e = tid; e < live * vecs; e += kThreads) {
-        const int row = e / vecs, d = e % vecs * 4;
-        float top = kNone;
-        for (int k = 0; k < splits; ++k)
-            top = fmaxf(top, part_load1(part, ((uint32_t)k * L::kSlotFloats + kTileRows * D + row) * 4));
-        const float ref = ref_of(top);
-        f32x4_t sum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        float weight = 0.f;
-        for (int k = 0; k < splits; ++k) {
-            const uint32_t slot = (uint32_t)k * L::kSlotFloats;
-            const float keep = exp2_fast(part_load1(part, (slot + kTileRows * D + row) * 4) - ref);
-            weight += keep * part_load1(part, (slot + kTileRows * D + kTileRows + row) * 4);
-            sum += part_load(part, (slot + row * D + d) * 4) * keep;
-        }
-        const int at = row0 + row, head = it.head * a.group + at % a.group;
-        const int64_t q_row = it.q0 + at / a.group;
-        store_row4<bf16_t>(a, q_row, head, d, sum, weight);
-        if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
-    }
+    if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
+    const auto region = [&](int w) { return w == 0 ? k_even : w == 1 ? v_even : w == 2 ? k_odd : v_odd; };
+    add_splits<bf16_t, D, kTileRows, kTileMaxSplits, 4>(a, it, splits, row0, min(kTileRows, rows - row0), part, region, sm);
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, 2) void stream_kernel(AttnArgs a, uint32_t *counters, float *slots) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void stream_kernel(AttnArgs a, uint32_t *counters, float *slots) {
     using S = Stream<T, D>;
     __shared__ __align__(16) unsigned char lds[kWaves][S::kWaveBytes];
     __shared__ StreamSmem sm;
@@ -709,7 +753,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles
     const int index = blockIdx.x;
     if (index < tiles)
         tile_item<D, kFull>(a, gridDim.x == (unsigned)tiles ? kTakeAll : kTakeLong, index, tiles, counters, slots,
-                            k_even, v_even, k_odd, v_odd, &sm.flag);
+                            k_even, v_even, k_odd, v_odd, sm);
     else
         stream_item<bf16_t, D>(a, kTakeShort, index - tiles, gridDim.x - tiles, counters + kMostSplits,
                                slots + (int64_t)kMostSplits * Tile<D>::kSlotFloats, k_even, v_even, k_odd, v_odd, sm);
