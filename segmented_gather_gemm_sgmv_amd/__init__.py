@@ -83,6 +83,11 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _kv_binding  # marshals the paged-cache calls; built with the library
+except ImportError as e:
+    raise ImportError(f"{_HERE / '_kv_binding.so'} is not built; run `python -m segmented_gather_gemm_sgmv_amd.build`") from e
+
 
 class SGMVError(RuntimeError):
     def __init__(self, fn: str, status: int):
@@ -114,7 +119,10 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle,
 
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
-        return _raw_stream(t.get_device())
+        index = t.get_device()
+        if index < 0:
+            raise ValueError("every tensor must be on a GPU device")
+        return _raw_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -502,42 +510,6 @@ SGMV_MAX_REQUESTS = 8192
 SGMV_ROPE_PLAIN, SGMV_ROPE_LINEAR, SGMV_ROPE_BY_PARTS = 0, 1, 2
 
 
-_I32 = torch.int32
-
-# These calls run once per layer or step on small operands, so the checks
-# below are kept to the attributes a bad call can get wrong, in one pass each.
-
-
-def _rows3(t: torch.Tensor, name: str, dtype, shape) -> Tuple[int, int]:
-    """(address, row stride in elements) of rows of heads [T, heads, head_dim]:
-    heads packed within a row, rows any distance apart."""
-    if t.dtype is not dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a {dtype} tensor on a GPU device")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    rows, heads, width = shape
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and width > 1) or (s1 != width and heads > 1):
-        raise ValueError(f"{name}: the heads of a row must be packed")
-    return t.data_ptr(), s0 if rows > 1 else heads * width
-
-
-def _ints(t: torch.Tensor, name: str, n: int) -> int:
-    if t.dtype is _I32 and t.is_cuda and t.is_contiguous() and t.numel() == n:
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on a GPU device")
-
-
-def _cache(K: torch.Tensor, V: torch.Tensor, dtype) -> torch.Size:
-    """(pages, kv_heads, page_size, head_dim) of a K/V cache pair."""
-    shape = K.shape
-    if (K.dtype is dtype and V.dtype is dtype and len(shape) == 4 and shape == V.shape and K.is_contiguous()
-            and V.is_contiguous() and K.is_cuda and V.is_cuda):
-        return shape
-    raise ValueError(f"K_cache and V_cache must be contiguous [pages, kv_heads, page_size, head_dim] {dtype} tensors "
-                     "of one shape on a GPU device")
-
-
 def sgmv_kv_tables(seq_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, page_size: int,
                    free_pages: torch.Tensor, pool_in: torch.Tensor, pool_out: torch.Tensor, q_start: torch.Tensor,
                    kv_len: torch.Tensor, position: torch.Tensor, slot: torch.Tensor, stream=None) -> None:
@@ -545,16 +517,8 @@ def sgmv_kv_tables(seq_len: torch.Tensor, new_len: torch.Tensor, block_table: to
     that add new_len >= 0 tokens get pages from the ring of free pages, ended
     ones (new_len < 0) give theirs back; q_start, kv_len, position, slot and
     pool_out are written (see include/sgmv.h). Nothing is read on the host."""
-    B, T = seq_len.numel(), slot.numel()
-    rows, width = block_table.shape
-    if rows != B:
-        raise ValueError("block_table must have one row per request")
-    st = lib.sgmv_kv_tables(_ints(seq_len, "seq_len", B), _ints(new_len, "new_len", B), B,
-                            _ints(block_table, "block_table", B * width), width, page_size,
-                            _ints(free_pages, "free_pages", free_pages.numel()), free_pages.numel(),
-                            _ints(pool_in, "pool_in", 4), _ints(pool_out, "pool_out", 4),
-                            _ints(q_start, "q_start", B + 1), _ints(kv_len, "kv_len", B),
-                            _ints(position, "position", T), _ints(slot, "slot", T), T, _stream(seq_len, stream))
+    st = _kv_binding.kv_tables(seq_len, new_len, block_table, page_size, free_pages, pool_in, pool_out, q_start, kv_len,
+                               position, slot, _stream(seq_len, stream))
     if st:
         raise SGMVError("sgmv_kv_tables", st)
 
@@ -581,57 +545,30 @@ def sgmv_rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k
     row stride; q_out may be q; q (with q_out) or k, v and the cache may be
     None. table: of sgmv_rope_table (its rot_dim elements of a head turn), or
     None to copy only."""
-    T = position.numel()
-    like = q if q is not None else k
-    if like is None:
-        raise ValueError("sgmv_rope_append needs q or k")
-    rows, heads, D = like.shape
-    if rows != T:
-        raise ValueError("q and k must have one row per token")
-    dtype = like.dtype
-    q_p = qo_p = k_p = v_p = K_p = V_p = slot_p = table_p = None
-    q_s = qo_s = k_s = v_s = q_heads = kv_heads = pages = rot_dim = 0
-    page, max_position = 16, 2 ** 31 - 1
-    if q is not None:
-        q_heads = heads
-        q_p, q_s = _rows3(q, "q", dtype, q.shape)
-        qo_p, qo_s = _rows3(q_out, "q_out", dtype, q.shape)
-    if k is not None:
-        pages, kv_heads, page, width = _cache(K_cache, V_cache, dtype)
-        shape = (T, kv_heads, width)
-        k_p, k_s = _rows3(k, "k", dtype, shape)
-        v_p, v_s = _rows3(v, "v", dtype, shape)
-        if width != D:
-            raise ValueError("q and the cache must agree in head_dim")
-        K_p, V_p, slot_p = K_cache.data_ptr(), V_cache.data_ptr(), _ints(slot, "slot", T)
-    if table is not None:
-        max_position, half, two = table.shape
-        if two != 2 or table.dtype is not torch.float32 or not table.is_cuda or not table.is_contiguous():
-            raise ValueError("table must be a contiguous float32 [max_position, rot_dim / 2, 2] tensor on a GPU device")
-        table_p, rot_dim = table.data_ptr(), 2 * half
-    st = lib.sgmv_rope_append(qo_p, qo_s, q_p, q_s, q_heads, k_p, k_s, v_p, v_s, K_p, V_p, pages, kv_heads, page, D,
-                              _ints(position, "position", T), slot_p, T, table_p, max_position, rot_dim,
-                              int(interleaved), _dtype_code(like), _stream(like, stream))
+    st = _kv_binding.rope_append(q_out, q, k, v, K_cache, V_cache, position, slot, table, interleaved,
+                                 _stream(position, stream))
     if st:
         raise SGMVError("sgmv_rope_append", st)
 
 
-_attention_workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
+_attention_workspaces: Dict[tuple, torch.Tensor] = {}
 
 
 def attention_workspace(device: torch.device, head_dim: int, dtype: torch.dtype, stream=None) -> torch.Tensor:
     """A zero-filled workspace for sgmv_paged_attention, cached per (device,
-    stream) and large enough for every head width and dtype given so far. It
-    is not the SGMV calls' workspace."""
+    stream, dtype, head width). It is not the SGMV calls' workspace."""
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     handle = _raw_stream(index) if stream is None else _torch_stream(device, stream).cuda_stream
-    ws = _attention_workspaces.get((index, handle))
-    nbytes = int(lib.sgmv_paged_attention_workspace_bytes(head_dim, _DTYPES[dtype]))
-    if ws is None or ws.numel() < nbytes:
+    key = (index, handle, dtype, head_dim)
+    ws = _attention_workspaces.get(key)
+    if ws is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+        nbytes = int(lib.sgmv_paged_attention_workspace_bytes(head_dim, _DTYPES[dtype]))
         with torch.cuda.device(index), torch.cuda.stream(_torch_stream(torch.device("cuda", index), stream)):
             ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{index}")
-        _attention_workspaces[index, handle] = ws
+        _attention_workspaces[key] = ws
     return ws
 
 
@@ -644,33 +581,14 @@ def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tens
     window > 0 only the last `window` keys and the first `sinks`. lse
     (optional, fp32 [T, q_heads]): log of the weights' sum. max_q_len: the
     largest number of new tokens of a request."""
-    dtype, shape = q.dtype, q.shape
-    T, heads, D = shape
-    q_p, q_s = _rows3(q, "q", dtype, shape)
-    out_p, out_s = _rows3(out, "out", dtype, shape)
-    pages, kv_heads, page, width = _cache(K_cache, V_cache, dtype)
-    if width != D:
-        raise ValueError("q and the cache must agree in head_dim")
-    B = kv_len.numel()
-    rows, blocks = block_table.shape
-    if rows != B:
-        raise ValueError("block_table must have one row per request")
-    lse_p = None
-    if lse is not None:
-        if lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (T, heads):
-            raise ValueError("lse must be a contiguous float32 [T, q_heads] tensor on a GPU device")
-        lse_p = lse.data_ptr()
     handle = _stream(q, stream)
-    code = _dtype_code(q)
     ws = workspace_buf
     if ws is None:
-        ws = _attention_workspaces.get((q.get_device(), handle))
-        if ws is None or ws.numel() < lib.sgmv_paged_attention_workspace_bytes(D, code):
-            ws = attention_workspace(q.device, D, dtype, stream)
-    st = lib.sgmv_paged_attention(out_p, out_s, lse_p, q_p, q_s, heads, K_cache.data_ptr(), V_cache.data_ptr(), pages,
-                                  kv_heads, page, D, _ints(block_table, "block_table", B * blocks), blocks,
-                                  _ints(q_start, "q_start", B + 1), _ints(kv_len, "kv_len", B), B, T, max_q_len, scale,
-                                  window, sinks, code, _dev(ws, "workspace"), ws.numel() * ws.element_size(), handle)
+        ws = _attention_workspaces.get((q.get_device(), handle, q.dtype, q.shape[-1]))
+        if ws is None:
+            ws = attention_workspace(q.device, q.shape[-1], q.dtype, stream)
+    st = _kv_binding.paged_attention(out, q, K_cache, V_cache, block_table, q_start, kv_len, scale, max_q_len, window,
+                                     sinks, lse, ws, handle)
     if st:
         raise SGMVError("sgmv_paged_attention", st)
     return out

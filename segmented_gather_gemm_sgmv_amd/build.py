@@ -4,7 +4,9 @@ Usage: ``python segmented_gather_gemm_sgmv_amd/build.py``.
 
 The kernel file is compiled once per rank (-DSGMV_RANK=8, 16, 32, 64) and
 once more for the rank dispatch and helper kernels; these objects, the paged
-cache's and the C ABI's compile in parallel, then link into one shared library.
+cache's and the C ABI's compile in parallel, then link into one shared library,
+against which the Python extension that marshals the paged-cache calls is
+linked.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libsgmv.so"
+BINDING = PKG / "_kv_binding.so"  # the paged-cache calls' argument marshalling (g++, torch's headers)
 
 KERNELS = CSRC / "sgmv_kernels.hip"
 API = CSRC / "sgmv_api.cpp"
@@ -46,6 +49,32 @@ def hipcc() -> str:
 
 def _messages(res) -> list:
     return [ln for ln in (res.stdout + res.stderr).splitlines() if NOISE not in ln]
+
+
+def _run(cmd, what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + "\n".join(_messages(res)))
+
+
+def build_binding(library: Path = LIBRARY, verbose: bool = False) -> Path:
+    """Compile the Python extension that marshals the paged-cache calls (no
+    device code), linked against `library` next to it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    inc = [f"-I{p}" for p in [INCLUDE, sysconfig.get_paths()["include"]] + list(include_paths())]
+    libs = [f"-L{p}" for p in [library.parent] + list(library_paths())]
+    tmp_out = BINDING.with_suffix(".so.tmp")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, str(CSRC / "kv_binding.cpp"),
+          "-o", str(tmp_out), *libs, f"-l:{library.name}", "-lc10", "-ltorch_cpu", "-ltorch_python",
+          "-Wl,-rpath,$ORIGIN"], "g++", verbose)
+    os.replace(tmp_out, BINDING)
+    return BINDING
 
 
 def build(output: Path = LIBRARY, extra_flags=(), verbose: bool = False, jobs: int = 0) -> Path:
@@ -82,12 +111,10 @@ def build(output: Path = LIBRARY, extra_flags=(), verbose: bool = False, jobs: i
         tmp_out = output.with_suffix(".so.tmp")
         cmd = [cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *extra_flags,
                *[str(u[2]) for u in units], "-o", str(tmp_out)]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("hipcc link failed:\n" + "\n".join(_messages(res)))
+        _run(cmd, "hipcc link", verbose)
     os.replace(tmp_out, output)
+    if output == LIBRARY:
+        build_binding(output, verbose)
     return output
 
 
