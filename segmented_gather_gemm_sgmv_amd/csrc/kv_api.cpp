@@ -168,6 +168,7 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
                            kv_heads,  page_shift(page_size), head_dim, block_table, max_blocks,
                            q_start,   kv_len,       num_requests, T,       max_q_len < T ? max_q_len : T,
                            scale,     window < far ? window : far, sinks < far ? sinks : far, dtype, workspace};
+    if (sgmv::attention_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_paged_attention(a, static_cast<hipStream_t>(stream)));
 }
 

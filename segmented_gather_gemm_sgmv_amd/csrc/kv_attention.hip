@@ -48,7 +48,9 @@ struct StreamSmem {
     int flag;
 };
 
-template <typename T, int D>
+// D: columns of a row in LDS; U: columns that products run over, at least
+// head_dim (96 for heads of 72 to 96 in rows of 128).
+template <typename T, int D, int U = D>
 struct Stream {
     static constexpr bool kBf16 = Elem<T>::kPerVec == 8;
     static constexpr int kBlocks = kBf16 ? 2 : 1;     // 16-key blocks per tile
@@ -56,7 +58,8 @@ struct Stream {
     static constexpr int kChunks = D / Elem<T>::kPerVec;  // 16-byte chunks per row
     static constexpr int kLoads = 16 * kChunks / 64;  // loads per lane and 16-key block
     static constexpr int kTileBytes = kKeys * kChunks * 16;
-    static constexpr int kOut = D / 16;               // 16-column blocks of the output
+    static constexpr int kUsed = U / Elem<T>::kPerVec;    // chunks that products run over
+    static constexpr int kOut = U / 16;               // 16-column blocks of the output
     static constexpr int kOutStride = D + 4;          // floats per row of the waves' results in LDS
     static constexpr int kOutBytes = 16 * kOutStride * 4;
     static constexpr int kWaveBytes = 2 * kTileBytes > kOutBytes ? 2 * kTileBytes : kOutBytes;  // one wave's LDS
@@ -203,11 +206,11 @@ __device__ __forceinline__ void add_splits(const AttnArgs &a, const Item &it, in
 // waves' own. kOnce: no other row tile reads the same keys, so they are loaded
 // past the caches' usual retention: at 64 heads on 8 and 512 requests of 128
 // to 4096 keys 785 -> 720 us, 5.8 -> 6.3 TB/s.
-template <typename T, int D, bool kOnce>
+template <typename T, int D, int U, bool kOnce>
 __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
                                             float *slots, unsigned char *lds0, unsigned char *lds1,
                                             unsigned char *lds2, unsigned char *lds3, StreamSmem &sm) {
-    using S = Stream<T, D>;
+    using S = Stream<T, D, U>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     Item it;
     if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMaxSplits, index,
@@ -229,12 +232,12 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int nch = a.head_dim / Elem<T>::kPerVec;
-    uint4 qf[CH / 4];
+    uint4 qf[S::kUsed / 4];
     {
         const T *q = static_cast<const T *>(a.q) + (int64_t)(it.q0 + (valid ? tok : 0)) * a.q_stride +
                      (int64_t)(valid ? q_head : 0) * a.head_dim;
 #pragma unroll
-        for (int k = 0; k < CH / 4; ++k) {
+        for (int k = 0; k < S::kUsed / 4; ++k) {
             const int c = 4 * k + g;
             const uint4 v = ld16(q + (c < nch ? c : 0) * Elem<T>::kPerVec);
             qf[k] = valid && c < nch ? v : make_uint4(0, 0, 0, 0);
@@ -320,7 +323,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
         for (int nb = 0; nb < NB; ++nb) {
             s[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < CH / 4; ++k) {
+            for (int k = 0; k < S::kUsed / 4; ++k) {
                 const uint4 kf = reinterpret_cast<const uint4 *>(k_lds)[S::k_slot(16 * nb + r, 4 * k + g)];
                 if constexpr (S::kBf16) {
                     s[nb] = mfma16(__builtin_bit_cast(bf16x8_t, kf), __builtin_bit_cast(bf16x8_t, qf[k]), s[nb]);
@@ -462,12 +465,13 @@ constexpr int kTileTarget = 512;   // as kStreamTarget
 constexpr int kTileMinChunk = 8;   // key tiles a split has about at least
 constexpr int kTileMaxSplits = 64; // of one group
 
-template <int D>
+template <int D, int U = D>
 struct Tile {
     static constexpr int kChunks = D / 8;
     static constexpr int kLoads = kTileKeys * kChunks / kThreads;  // per thread, of K and of V
     static constexpr int kBytes = kTileKeys * kChunks * 16;
-    static constexpr int kOut = D / 32;                            // 32-column blocks of the output
+    static constexpr int kSteps = U / 16;                          // 16-column steps of the scores
+    static constexpr int kOut = U / 32;                            // 32-column blocks of the output
     static constexpr int kSlotFloats = kTileRows * D + 2 * kTileRows;
 };
 
@@ -505,12 +509,12 @@ __device__ __forceinline__ void loads_barrier() {
     lds_barrier();
 }
 
-// kFull: head_dim is D (no chunk of a row is past the head).
-template <int D, bool kFull>
+// U as for Stream; kFull: head_dim is D.
+template <int D, int U, bool kFull>
 __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
                                           float *slots, unsigned char *k_even, unsigned char *v_even,
                                           unsigned char *k_odd, unsigned char *v_odd, StreamSmem &sm) {
-    using L = Tile<D>;
+    using L = Tile<D, U>;
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
@@ -534,12 +538,12 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0;
     const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
     const int head_dim = kFull ? D : a.head_dim, nch = head_dim / 8;
-    bf16x8_t qf[CH / 2];
+    bf16x8_t qf[L::kSteps];
     {
         const bf16_t *q = static_cast<const bf16_t *>(a.q) + (int64_t)(it.q0 + (valid ? tok : 0)) * a.q_stride +
                           (int64_t)(valid ? q_head : 0) * a.head_dim;
 #pragma unroll
-        for (int k = 0; k < CH / 2; ++k) {
+        for (int k = 0; k < L::kSteps; ++k) {
             const int c = 2 * k + h;
             const uint4 v = ld16(q + (c < nch ? c : 0) * 8);
             qf[k] = __builtin_bit_cast(bf16x8_t, valid && c < nch ? v : make_uint4(0, 0, 0, 0));
@@ -596,9 +600,9 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 
     // Offsets of this lane's fragments in a buffer's first rows: K rows r (32 of a product), chunk 2 k + h; V rows
     // 4 h + 0..3, columns 32 d + 16 (lane / 16 % 2) + 0..15. Sixteen rows further on the swizzles are the same.
-    uint32_t k_at[CH / 2], v_at[L::kOut];
+    uint32_t k_at[L::kSteps], v_at[L::kOut];
 #pragma unroll
-    for (int k = 0; k < CH / 2; ++k) k_at[k] = S::k_slot(r, 2 * k + h) * 16;
+    for (int k = 0; k < L::kSteps; ++k) k_at[k] = S::k_slot(r, 2 * k + h) * 16;
 #pragma unroll
     for (int d = 0; d < L::kOut; ++d)
         v_at[d] = S::v_slot(4 * h + ((lane & 15) >> 2), 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) * 16 +
@@ -622,12 +626,12 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             lds_barrier();
         }
         if (live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks)) {
-            bf16x8_t kf[2][CH / 2];
+            bf16x8_t kf[2][L::kSteps];
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) kf[0][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k]);
+            for (int k = 0; k < L::kSteps; ++k) kf[0][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) kf[1][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k] + 32 * CH * 16);
+            for (int k = 0; k < L::kSteps; ++k) kf[1][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k] + 32 * CH * 16);
             __builtin_amdgcn_sched_barrier(0);
             f32x16_t s[2];
 #pragma unroll
@@ -635,9 +639,9 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) s[0] = mfma32(kf[0][k], qf[k], s[0]);
+            for (int k = 0; k < L::kSteps; ++k) s[0] = mfma32(kf[0][k], qf[k], s[0]);
 #pragma unroll
-            for (int k = 0; k < CH / 2; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
+            for (int k = 0; k < L::kSteps; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
             bf16x8_t vf[2][L::kOut];  // V fragments of two 16-key steps
 #pragma unroll
             for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(vb + v_at[d], 8 * CH * 16);
@@ -735,18 +739,18 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <typename T, int D, bool kOnce>
+template <typename T, int D, int U, bool kOnce>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void stream_kernel(AttnArgs a, uint32_t *counters, float *slots) {
-    using S = Stream<T, D>;
+    using S = Stream<T, D, U>;
     __shared__ __align__(16) unsigned char lds[kWaves][S::kWaveBytes];
     __shared__ StreamSmem sm;
-    stream_item<T, D, kOnce>(a, kTakeAll, blockIdx.x, gridDim.x, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
+    stream_item<T, D, U, kOnce>(a, kTakeAll, blockIdx.x, gridDim.x, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
 }
 
 // Workgroups below `tiles` take the tile items, the others the streaming
 // items, each with counters and slots of its own: in a batch of both, the
 // ones compute while the others read.
-template <int D, bool kFull>
+template <int D, int U, bool kFull>
 __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles, uint32_t *counters, float *slots) {
     // Two buffers of K and V. They are variables of their own, and the loop names them statically, so that the
     // compiler sees that a buffer's loads in flight have nothing to do with reads of the other one.
@@ -755,10 +759,10 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles
     __shared__ StreamSmem sm;
     const int index = blockIdx.x;
     if (index < tiles)
-        tile_item<D, kFull>(a, gridDim.x == (unsigned)tiles ? kTakeAll : kTakeLong, index, tiles, counters, slots,
+        tile_item<D, U, kFull>(a, gridDim.x == (unsigned)tiles ? kTakeAll : kTakeLong, index, tiles, counters, slots,
                             k_even, v_even, k_odd, v_odd, sm);
     else
-        stream_item<bf16_t, D, true>(a, kTakeShort, index - tiles, gridDim.x - tiles, counters + kMostSplits,
+        stream_item<bf16_t, D, U, true>(a, kTakeShort, index - tiles, gridDim.x - tiles, counters + kMostSplits,
                                slots + (int64_t)kMostSplits * Tile<D>::kSlotFloats, k_even, v_even, k_odd, v_odd, sm);
 }
 
@@ -777,18 +781,30 @@ int64_t most_groups(const AttnArgs &a, int64_t requests, int rows) {
     return per * requests < by_rows ? per * requests : by_rows;
 }
 
-uint32_t *counters_of(const AttnArgs &a) { return static_cast<uint32_t *>(a.workspace); }
-float *slots_of(const AttnArgs &a) { return reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes); }
+// A launch: workgroups for tile items, then for streaming items.
+struct Grid {
+    int64_t tiles, streams;
+};
+
+Grid grid_of(const AttnArgs &a) {
+    if (a.dtype != SGMV_BF16) return {0, most_groups(a, a.num_requests, kStreamRows) * a.kv_heads + kStreamTarget};
+    // A batch whose requests all fit one row tile of the streaming kernel is its alone.
+    const int64_t one_each = (int64_t)a.num_requests * a.kv_heads + kStreamTarget;
+    if ((int64_t)a.max_q_len * a.group <= kShortRows) return {0, one_each};
+    // Otherwise requests go to the two kinds of items by their rows. At most T * group / (kShortRows + 1) are long; a
+    // batch of one request has tile items only.
+    const int64_t could = (int64_t)a.T * a.group / (kShortRows + 1);
+    const bool one = a.num_requests == 1;
+    const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
+    return {most_groups(a, longs, kTileRows) * a.kv_heads + kTileTarget, one ? 0 : one_each};
+}
 
 template <typename T>
-hipError_t launch_stream(const AttnArgs &a, int64_t groups, hipStream_t st) {
-    const int64_t grid = groups * a.kv_heads + kStreamTarget;
-    if (grid > (int64_t)1 << 24) return hipErrorInvalidValue;
+auto stream_kernel_of(const AttnArgs &a) {
     const bool once = (int64_t)a.max_q_len * a.group <= kStreamRows;  // a request is one row tile
-    const auto kernel = a.head_dim <= 64 ? (once ? stream_kernel<T, 64, true> : stream_kernel<T, 64, false>)
-                                         : (once ? stream_kernel<T, 128, true> : stream_kernel<T, 128, false>);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), 0, st, a, counters_of(a), slots_of(a));
-    return hipGetLastError();
+    if (a.head_dim <= 64) return once ? stream_kernel<T, 64, 64, true> : stream_kernel<T, 64, 64, false>;
+    if (a.head_dim <= 96) return once ? stream_kernel<T, 128, 96, true> : stream_kernel<T, 128, 96, false>;
+    return once ? stream_kernel<T, 128, 128, true> : stream_kernel<T, 128, 128, false>;
 }
 
 }  // namespace
@@ -800,24 +816,27 @@ size_t attention_workspace_bytes(int head_dim, int dtype) {
     return kCounterBytes + (size_t)kMostSplits * (stream + tile) * sizeof(float);
 }
 
+int64_t attention_workgroups(const AttnArgs &a) {
+    const Grid g = grid_of(a);
+    return g.tiles + g.streams;
+}
+
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-    if (a.dtype != SGMV_BF16) return launch_stream<float>(a, most_groups(a, a.num_requests, kStreamRows), st);
-    // A batch whose requests all fit one row tile of the streaming kernel is its alone.
-    if ((int64_t)a.max_q_len * a.group <= kShortRows) return launch_stream<bf16_t>(a, a.num_requests, st);
-    // Otherwise requests go to the two kinds of items by their rows. At most T * group / (kShortRows + 1) are long; a
-    // batch of one request has tile items only.
-    const int64_t could = (int64_t)a.T * a.group / (kShortRows + 1);
-    const bool one = a.num_requests == 1;
-    const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
-    const int64_t tiles = most_groups(a, longs, kTileRows) * a.kv_heads + kTileTarget;
-    const int64_t streams = one ? 0 : (int64_t)a.num_requests * a.kv_heads + kStreamTarget;
-    if (tiles + streams > (int64_t)1 << 24) return hipErrorInvalidValue;
-    const auto kernel = a.head_dim == 64    ? tile_kernel<64, true>
-                        : a.head_dim == 128 ? tile_kernel<128, true>
-                        : a.head_dim < 64   ? tile_kernel<64, false>
-                                            : tile_kernel<128, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles + streams)), dim3(kThreads), 0, st, a, (int)tiles, counters_of(a),
-                       slots_of(a));
+    uint32_t *counters = static_cast<uint32_t *>(a.workspace);
+    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
+    const Grid g = grid_of(a);
+    const dim3 grid((unsigned)(g.tiles + g.streams));
+    if (g.tiles == 0) {
+        const auto kernel = a.dtype == SGMV_BF16 ? stream_kernel_of<bf16_t>(a) : stream_kernel_of<float>(a);
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a, counters, slots);
+    } else {
+        const auto kernel = a.head_dim == 64    ? tile_kernel<64, 64, true>
+                            : a.head_dim == 128 ? tile_kernel<128, 128, true>
+                            : a.head_dim < 64   ? tile_kernel<64, 64, false>
+                            : a.head_dim <= 96  ? tile_kernel<128, 96, false>
+                                                : tile_kernel<128, 128, false>;
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a, (int)g.tiles, counters, slots);
+    }
     return hipGetLastError();
 }
 

@@ -72,6 +72,8 @@ constexpr int kMostSplits = 1024;
 // slots of the launch that splits the most.
 size_t attention_workspace_bytes(int head_dim, int dtype);
 
+int64_t attention_workgroups(const AttnArgs &a);  // of its launch
+
 hipError_t launch_kv_tables(const TablesArgs &a, hipStream_t st);
 hipError_t launch_rope_table(const RopeTableArgs &a, hipStream_t st);
 hipError_t launch_rope_append(const RopeArgs &a, hipStream_t st);

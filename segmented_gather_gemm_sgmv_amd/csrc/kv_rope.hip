@@ -71,13 +71,13 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a, int r
     }
     if (is_v || part >= rot_units) {
         const int at = is_v ? part * kVec : a.rot_dim + (part - rot_units) * kVec;
-        st16(dst + at, ld16(src + at));
+        st16(dst + at, ld16_stream(src + at));
         return;
     }
     const int first = a.interleaved ? part * 2 * kVec : part * kVec;
     const int second = first + (a.interleaved ? kVec : a.rot_dim / 2);
     float x[2 * kVec], y[2 * kVec], cs[2 * kVec];
-    const uint4 lo = ld16(src + first), hi = ld16(src + second);
+    const uint4 lo = ld16_stream(src + first), hi = ld16_stream(src + second);
     const float *turn = a.table + ((int64_t)pos * (a.rot_dim / 2) + part * kVec) * 2;
 #pragma unroll
     for (int i = 0; i < 2 * kVec; i += 4) widen<float>(ld16(turn + i), reinterpret_cast<float(&)[4]>(cs[i]));
