@@ -3,7 +3,9 @@
 
 Argument marshalling only: every function below checks tensor placement,
 dtype and contiguity, passes raw device pointers, sizes and the current HIP
-stream to the C function of the same name, and raises on a non-zero status.
+stream to the C function of the same name, and raises on a non-zero status
+(the calls of the paged key/value cache through a small compiled module,
+``_kv_binding.so``, the others through ctypes).
 All arithmetic runs in the library's gfx950 kernels. PyTorch supplies device
 memory and streams.
 
@@ -594,6 +596,68 @@ def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tens
     return out
 
 
+class PagedKVCache:
+    """Paged K and V of one or more layers, with the one block table, the ring
+    of free pages and the lengths that their requests share; all of it on the
+    device, carried from step to step without the host reading it.
+
+    A step: ``step`` (slots for the step's new tokens, ended requests' pages
+    back), then per layer ``append`` and ``attend``. Requests are the rows
+    0 .. max_requests - 1; one that ended is free for another at once, its
+    pages from the next step on. Lengths and pool are kept twice and change
+    places at every step, so a step is captured in a graph two at a time."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_requests: int,
+                 max_blocks: int, num_layers: int = 1, dtype=torch.bfloat16, device="cuda"):
+        self.page_size = page_size
+        shape = (num_layers, num_pages, kv_heads, page_size, head_dim)
+        self.K, self.V = torch.zeros(shape, dtype=dtype, device=device), torch.zeros(shape, dtype=dtype, device=device)
+
+        def ints(*size):
+            return torch.zeros(size, dtype=torch.int32, device=device)
+
+        self.block_table = ints(max_requests, max_blocks).fill_(-1)
+        self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=device)
+        self._len, self._pool = [ints(max_requests), ints(max_requests)], [ints(4), ints(4)]
+        self._pool[0][1] = num_pages
+        self.q_start = ints(max_requests + 1)
+        self.position = self.slot = ints(0)
+
+    @property
+    def kv_len(self) -> torch.Tensor:
+        """Tokens each request has in the cache, the last step's included."""
+        return self._len[0]
+
+    @property
+    def pool(self) -> torch.Tensor:
+        """[ring's first entry, free pages, requests the last step refused, its tokens]."""
+        return self._pool[0]
+
+    def step(self, new_len: torch.Tensor, num_tokens: int, stream=None) -> None:
+        """The next step: request b adds new_len[b] tokens (num_tokens in all),
+        or has ended (new_len[b] < 0). Sets q_start, kv_len, position, slot."""
+        if self.slot.numel() != num_tokens:
+            with torch.cuda.stream(_torch_stream(self.slot.device, stream)):
+                self.position = torch.empty(num_tokens, dtype=torch.int32, device=self.slot.device)
+                self.slot = torch.empty_like(self.position)
+        sgmv_kv_tables(self._len[0], new_len, self.block_table, self.page_size, self.free_pages, self._pool[0],
+                       self._pool[1], self.q_start, self._len[1], self.position, self.slot, stream)
+        self._len.reverse()
+        self._pool.reverse()
+
+    def append(self, q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+               table: Optional[torch.Tensor], interleaved: bool = False, layer: int = 0, stream=None) -> None:
+        """q_out = q rotated; k (rotated) and v of the step's tokens to the cache."""
+        sgmv_rope_append(q_out, q, k, v, self.K[layer], self.V[layer], self.position, self.slot, table, interleaved,
+                         stream)
+
+    def attend(self, out: torch.Tensor, q: torch.Tensor, scale: float, max_q_len: int, window: int = 0,
+               sinks: int = 0, lse: Optional[torch.Tensor] = None, layer: int = 0, stream=None) -> torch.Tensor:
+        """out = attention of the step's tokens over what their requests have cached."""
+        return sgmv_paged_attention(out, q, self.K[layer], self.V[layer], self.block_table, self.q_start, self.kv_len,
+                                    scale, max_q_len, window, sinks, lse, stream=stream)
+
+
 def sgmv_version() -> int:
     return int(lib.sgmv_version())
 
@@ -604,6 +668,6 @@ __all__ = ["sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_shrink_gather", "sg
            "sgmv_workspace_bytes", "sgmv_build_segments",
            "sgmv_pool_pointers", "sgmv_version", "workspace", "SGMVError", "lib", "EXPORTS",
            "LIBRARY", "SGMV_F32", "SGMV_BF16", "sgmv_workspace_status", "sgmv_set_wait_limit",
-           "sgmv_kv_tables", "sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "attention_workspace",
+           "sgmv_kv_tables", "sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "attention_workspace", "PagedKVCache",
            "SGMV_MAX_REQUESTS", "SGMV_ROPE_PLAIN", "SGMV_ROPE_LINEAR", "SGMV_ROPE_BY_PARTS",
            "SGMV_WS_WAIT_TIMEOUT", "SGMV_WS_BAD_OFFSETS", "sgmv_fused_noalloc", "SGMV_NOALLOC_SCRATCH_BYTES"]

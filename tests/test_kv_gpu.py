@@ -488,3 +488,26 @@ def test_graph_of_a_step(dev):
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
         assert float(out.float().sum()) == float(want.float().sum())
+
+
+# -- the operators together ---------------------------------------------------------
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_serving_layer_against_dense(dev, dtype, window):
+    """examples/lora_attention_layer.py: prompts, single tokens, ended requests
+    and new ones in their place, with adapters, against a dense recomputation.
+
+    fp32: every stage's sums of up to 256 terms are off by at most 256 2^-24 of
+    their terms' sizes, and some eight such stages follow one another. bf16:
+    eight roundings of 2^-8 on the way (projections, deltas, rotation, weights,
+    output), those before the softmax acting through scores of order one."""
+    import importlib.util
+    from pathlib import Path
+    spec = importlib.util.spec_from_file_location(
+        "lora_attention_layer", Path(__file__).resolve().parents[1] / "examples" / "lora_attention_layer.py")
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(256, 8, 2, 64, 16, 4, 6, 64, 16, 256, dtype, dev, window, 3)
+    worst, seconds = example.serve(layer, 256, 6, 14, 60)
+    assert len(seconds) == 14
+    assert worst <= (2.0 ** -4 if dtype is BF16 else 8 * 256 * 2.0 ** -24), worst
