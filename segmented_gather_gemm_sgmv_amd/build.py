@@ -19,7 +19,8 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
-CSRC = PKG / "csrc"
+CSRC = PKG / "csrc"        # SGMV
+CSRC_KV = PKG / "csrc_kv"  # the paged key/value cache
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libsgmv.so"
 BINDING = PKG / "_kv_binding.so"  # the paged-cache calls' argument marshalling (g++, torch's headers)
@@ -27,7 +28,7 @@ BINDING = PKG / "_kv_binding.so"  # the paged-cache calls' argument marshalling 
 KERNELS = CSRC / "sgmv_kernels.hip"
 API = CSRC / "sgmv_api.cpp"
 HOST = CSRC / "sgmv_host.cpp"  # host-only entry points (no HIP): also built alone with the sanitizers
-KV = [CSRC / "kv_api.cpp", CSRC / "kv_tables.hip", CSRC / "kv_rope.hip", CSRC / "kv_attention.hip"]  # the paged cache
+KV = [CSRC_KV / n for n in ("kv_api.cpp", "kv_tables.hip", "kv_rope.hip", "kv_attention.hip")]
 SOURCES = [KERNELS, API, HOST, *KV]
 RANKS = (8, 16, 32, 64)
 ARCH = "gfx950"
@@ -70,7 +71,7 @@ def build_binding(library: Path = LIBRARY, verbose: bool = False) -> Path:
     libs = [f"-L{p}" for p in [library.parent] + list(library_paths())]
     tmp_out = BINDING.with_suffix(".so.tmp")
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, str(CSRC / "kv_binding.cpp"),
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, str(CSRC_KV / "kv_binding.cpp"),
           "-o", str(tmp_out), *libs, f"-l:{library.name}", "-lc10", "-ltorch_cpu", "-ltorch_python",
           "-Wl,-rpath,$ORIGIN"], "g++", verbose)
     os.replace(tmp_out, BINDING)

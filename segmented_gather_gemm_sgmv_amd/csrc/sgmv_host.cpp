@@ -18,7 +18,7 @@ using namespace sgmv::abi;
 
 extern "C" {
 
-int sgmv_version(void) { return 400; }
+int sgmv_version(void) { return 300; }
 
 const char *sgmv_status_string(int status) {
     switch (status) {
@@ -27,7 +27,7 @@ const char *sgmv_status_string(int status) {
         case SGMV_ERR_SHAPE: return "invalid size (negative, not a multiple of 8, or too large)";
         case SGMV_ERR_RANK: return "rank must be 8, 16, 32 or 64";
         case SGMV_ERR_DTYPE: return "dtype must be SGMV_F32 or SGMV_BF16";
-        case SGMV_ERR_ALIGN: return "an operand must be 16-byte aligned";
+        case SGMV_ERR_ALIGN: return "X, Y and V must be 16-byte aligned";
         case SGMV_ERR_WORKSPACE: return "workspace missing or too small";
         case SGMV_ERR_HIP: return "HIP runtime error at launch";
         case SGMV_ERR_ADAPTER: return "adapter id negative or outside the pool";
