@@ -111,7 +111,7 @@ __device__ __forceinline__ V wave_scan(V v) {
 // lengths are read at once.
 template <int kRows, int kKeys, int kBatch>
 __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
-                                             int max_splits, int index, int grid, Item &it) {
+                                             int min_tiles, int max_splits, int index, int grid, Item &it) {
     const int lane = threadIdx.x & 63, B = a.num_requests;
     const int per = kBatch == 1 ? 1 : (B + 63) / 64, first = lane * per;
     Share s[kBatch];
@@ -134,7 +134,9 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
 
     // A group is split where it is at least one and a half chunks long; the
     // groups that are split then have at most 4/3 * target parts together.
-    const auto splits_of = [&](const Share &x) { return min(max((x.tiles + chunk / 2) / chunk, 1), max_splits); };
+    const auto splits_of = [&](const Share &x) {
+        return x.tiles < min_tiles ? 1 : min(max((x.tiles + chunk / 2) / chunk, 1), max_splits);
+    };
     int items = 0, slots = 0;
     for (int j0 = 0; j0 < per; j0 += kBatch) {
         if (per > kBatch) read(j0);
@@ -182,10 +184,10 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
 
 template <int kRows, int kKeys>
 __device__ __forceinline__ bool find_item(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
-                                          int max_splits, int index, int grid, Item &it) {
+                                          int min_tiles, int max_splits, int index, int grid, Item &it) {
     return a.num_requests <= 64
-               ? find_item_of<kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, max_splits, index, grid, it)
-               : find_item_of<kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, max_splits, index, grid, it);
+               ? find_item_of<kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
+               : find_item_of<kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
 }
 
 // Maximum and sum over the four lanes (l, l ^ 16, l ^ 32, l ^ 48) that hold

@@ -37,7 +37,8 @@ constexpr float kSlack = 8.f;
 // ----------------------------------------------------------------------------
 constexpr int kStreamRows = 16;
 constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
-constexpr int kStreamMinChunk = 16;  // key tiles a split has about at least (four per wave)
+constexpr int kStreamMinChunk = 8;   // key tiles a split has about at least (two per wave)
+constexpr int kStreamMinTiles = 24;  // of a group that is split: fewer are done before the parts would be added up
 constexpr int kStreamMaxSplits = 256;  // of one group
 
 constexpr int kShortRows = 16;       // bf16 groups up to this many rows; longer ones go to the tile kernel
@@ -127,13 +128,14 @@ __device__ __forceinline__ float lse_of(float m, float weight) {
 // The last of a group's items to arrive adds the splits up, in their order.
 // Slots hold kRows x D sums, then the rows' maxima, then their weight sums.
 // All of the maxima are read first, each thread's in one go, and the splits'
-// factors left in LDS; then the sums, kAtOnce 4-column pieces and four splits
+// factors left in LDS; then the sums, kAtOnce 4-column pieces and kDeep splits
 // at a time: what this costs is the latency of reads from other XCDs, so as
 // many as possible are in flight.
 template <typename T, int D, int kRows, int kMaxSplits, int kAtOnce, typename Region>
 __device__ __forceinline__ void add_splits(const AttnArgs &a, const Item &it, int splits, int row0, int live,
                                            __amdgpu_buffer_rsrc_t part, const Region &region, StreamSmem &sm) {
     constexpr int kSlot = kRows * D + 2 * kRows, kParts = kThreads / kRows, kEach = kMaxSplits / kParts;
+    constexpr int kDeep = 16 / kAtOnce;  // splits read at a time
     const int tid = threadIdx.x;
     const auto factor = [&](int row) {  // splits' factors of a row, kMaxSplits apart
         return reinterpret_cast<float *>(region(row / (kRows / kWaves))) + row % (kRows / kWaves) * kMaxSplits;
@@ -188,10 +190,23 @@ __device__ __forceinline__ void add_splits(const AttnArgs &a, const Item &it, in
             f[u] = factor(e / vecs);
             at[u] = (e / vecs * D + e % vecs * 4) * 4;
         }
-#pragma unroll 16 / kAtOnce
-        for (int k = 0; k < splits; ++k)
+        const auto add = [&](int k0, auto deep) {  // splits k0 .. k0 + deep - 1, as far as there are
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) sum[u] += part_load(part, (uint32_t)k * kSlot * 4 + at[u]) * f[u][k];
+            for (int j = 0; j < deep(); ++j) {
+                const int k = min(k0 + j, splits - 1);
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const f32x4_t x = part_load(part, (uint32_t)k * kSlot * 4 + at[u]) * f[u][k];
+                    sum[u] += k0 + j < splits ? x : f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+            }
+        };
+        for (int k0 = 0; k0 < splits; k0 += kDeep) {
+            if (splits - k0 > kDeep / 4)
+                add(k0, [] { return kDeep; });
+            else
+                add(k0, [] { return kDeep / 4; });
+        }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             const int e = e0 + u * kThreads;
@@ -213,7 +228,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     using S = Stream<T, D, U>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     Item it;
-    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMaxSplits, index,
+    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
                                               grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
@@ -463,6 +478,7 @@ constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr int kTileTarget = 512;   // as kStreamTarget
 constexpr int kTileMinChunk = 8;   // key tiles a split has about at least
+constexpr int kTileMinTiles = 12;  // of a group that is split
 constexpr int kTileMaxSplits = 64; // of one group
 
 template <int D, int U = D>
@@ -518,7 +534,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
-    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMaxSplits, index, grid, it)) return;
+    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
     const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
