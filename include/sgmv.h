@@ -475,7 +475,8 @@ int sgmv_rope_table(float *table, int32_t max_position, int32_t rot_dim, double 
  *
  * q_out        out, [T][q_heads][head_dim] with its own row stride; may be q.
  * table        of sgmv_rope_table; not read (may be NULL) when rot_dim is 0.
- * rot_dim      a multiple of 16, 0 .. head_dim.
+ * rot_dim      even, 0 .. head_dim (multiples of 16 in bf16 and of 8 in fp32 move
+ *              16 bytes at a time, others less).
  * position     device int32[T]; a token whose position is outside
  *              [0, max_position) is left out (nothing of it is written).
  * slot         device int32[T]; a token without a slot (or one outside the

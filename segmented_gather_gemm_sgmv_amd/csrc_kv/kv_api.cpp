@@ -97,11 +97,8 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
                      int32_t max_position, int32_t rot_dim, int32_t interleaved, int32_t dtype, void *stream) {
     if (!valid_dtype(dtype)) return SGMV_ERR_DTYPE;
     if (T < 0 || q_heads < 0 || kv_heads < 0 || max_position < 0 || !valid_head(head_dim)) return SGMV_ERR_SHAPE;
-    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0) return SGMV_ERR_SHAPE;
-    // one 256-thread workgroup per token and 256 units of 8 or more elements
-    if ((int64_t)q_heads + kv_heads > 65536 ||
-        ((int64_t)q_heads + 2 * (int64_t)kv_heads) * head_dim / 4 / 256 + 1 > sgmv::kMaxWorkgroups / (T > 0 ? T : 1))
-        return SGMV_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0) return SGMV_ERR_SHAPE;
+    if ((int64_t)q_heads + kv_heads > 65536) return SGMV_ERR_SHAPE;
     int st = kv_heads > 0 ? check_pages(num_pages, page_size) : (int)SGMV_OK;
     if (st != SGMV_OK) return st;
     if (T == 0 || q_heads + kv_heads == 0) return SGMV_OK;
@@ -124,6 +121,7 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
                            k_stride,  v,            v_stride,   K_cache,   V_cache,   num_pages,
                            kv_heads,  kv_heads > 0 ? page_shift(page_size) : 4, head_dim, position, slot, T,
                            table,     max_position, rot_dim,    interleaved, dtype};
+    if (sgmv::rope_append_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_rope_append(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -76,6 +76,7 @@ int64_t attention_workgroups(const AttnArgs &a);  // of its launch
 
 hipError_t launch_kv_tables(const TablesArgs &a, hipStream_t st);
 hipError_t launch_rope_table(const RopeTableArgs &a, hipStream_t st);
+int64_t rope_append_workgroups(const RopeArgs &a);
 hipError_t launch_rope_append(const RopeArgs &a, hipStream_t st);
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st);
 

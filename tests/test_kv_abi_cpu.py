@@ -36,7 +36,7 @@ def test_rope_refusals():
     for k in ("q_out", "q", "k", "v", "K", "V", "position", "slot", "table"):
         assert rope(**{k: None}) == NULL, k
     for bad in (dict(T=-1), dict(hq=-1), dict(hk=-1), dict(D=0), dict(D=12), dict(D=136), dict(rot=-16), dict(rot=144),
-                dict(rot=8), dict(rot=40), dict(page=17), dict(pages=0), dict(qs=1016), dict(qos=0), dict(ks=255),
+                dict(rot=7), dict(rot=41), dict(page=17), dict(pages=0), dict(qs=1016), dict(qos=0), dict(ks=255),
                 dict(vs=128), dict(max_position=-1), dict(T=(1 << 24) + 1), dict(hq=70000, qs=1 << 24, qos=1 << 24)):
         assert rope(**bad) == SHAPE, bad
     for bad in (dict(q=P[1] + 8), dict(q_out=P[0] + 2), dict(k=P[2] + 4), dict(v=P[3] + 8), dict(K=P[4] + 8),

@@ -170,7 +170,10 @@ def rope_case(rng, dev, T, hq, hk, D, dtype, page, pages, max_position, fused=Tr
 @pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
 @pytest.mark.parametrize("T,hq,hk,D,rot,page", [(1, 8, 1, 128, 128, 16), (7, 32, 32, 128, 128, 16), (65, 5, 5, 80, 32, 32),
                                                 (33, 14, 2, 64, 64, 64), (3, 1, 1, 16, 16, 16), (130, 6, 3, 72, 48, 128),
-                                                (20, 4, 2, 96, 0, 16), (9, 71, 1, 64, 16, 256)])
+                                                (20, 4, 2, 96, 0, 16), (9, 71, 1, 64, 16, 256),
+                                                # rotated parts of every run length
+                                                (11, 4, 2, 80, 40, 16), (8, 3, 1, 64, 36, 32), (8, 2, 2, 40, 2, 16),
+                                                (7, 5, 5, 128, 126, 16), (10, 6, 2, 24, 24, 16)])
 def test_rope_append(dev, dtype, interleaved, T, hq, hk, D, rot, page):
     rng = np.random.default_rng(T * 7 + D)
     n = 999
