@@ -34,6 +34,18 @@ constexpr float kSlack = 8.f;
 // goes through the wave's own LDS region into the matrix instructions' layout,
 // with no barrier in the loop. 16 rows go through v_mfma_*_16x16: with fewer
 // rows the rest of the tile is idle, which costs nothing that HBM would not.
+// Two workgroups fit a CU; their eight waves keep 128 KB in flight.
+//
+// Measured, bf16, heads of 128: 512 requests of 128 to 4096 keys, 64 heads on
+// 8, 716 us (6.4 TB/s); 64 requests of 1 to 2048 keys, 32 heads, 161 us
+// (6.2 TB/s); one request of 131001 keys, 64 heads on 8, 64 splits a head,
+// 92 us (5.8 TB/s); a plain streaming read reaches 5.5 to 5.9 TB/s without
+// the streaming hint. Where there is too little work to fill the GPU a wave's
+// further tile costs 1.1 us (its loads' latency), and adding splits up 2.5:
+// kStreamMinChunk and kStreamMinTiles follow from that (one request of 2000
+// keys: 13.2 us in splits of 16 tiles, 11.0 in splits of 8).
+// fp32 chunks (16 rows at a time): 79 TFLOP/s at 4 x 256 tokens, 32 heads on
+// 8, of the 155 that a large fp32 product reaches.
 // ----------------------------------------------------------------------------
 constexpr int kStreamRows = 16;
 constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
@@ -41,7 +53,10 @@ constexpr int kStreamMinChunk = 8;   // key tiles a split has about at least (tw
 constexpr int kStreamMinTiles = 24;  // of a group that is split: fewer are done before the parts would be added up
 constexpr int kStreamMaxSplits = 256;  // of one group
 
-constexpr int kShortRows = 16;       // bf16 groups up to this many rows; longer ones go to the tile kernel
+// bf16 requests of up to this many packed rows, two row tiles, are streamed; longer ones go to the tile kernel.
+// Measured streamed and tiled, 2000 keys, 64 heads on 8: 24 rows 15.8 and 20.9 us (4 requests), 45.9 and 50.3 (32);
+// 32 heads of their own: 32 rows 29.5 and 31.5 (4), 200 and 190 (32); 64 heads on 8: 64 rows 17.6 and 25.2, 67.8 and 61.
+constexpr int kShortRows = 32;
 
 struct StreamSmem {
     float m[kWaves][16], l[kWaves][16];  // the waves' running maxima and sums
@@ -467,12 +482,24 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 // ----------------------------------------------------------------------------
 // Tile kernel: bf16 groups of many rows (prompt chunks).
 //
-// What bounds it: the matrix cores. A workgroup takes 128 packed rows, 32 per
-// wave, against key tiles of 64 that its waves share: the next tile is loaded
-// into registers while the present one is worked on from LDS, then written to
-// the other of two LDS buffers, one barrier per tile. 32 rows go through
-// v_mfma_f32_32x32x16_bf16, whose transposed scores leave half of a row's keys
-// on each of two lanes.
+// What bounds it: the matrix cores, and the power they and their operands
+// take. A workgroup takes 128 packed rows, 32 per wave, against key tiles of
+// 64 that its waves share: the next tile is loaded straight to the other of
+// two LDS buffers while the present one is worked on, one barrier per tile.
+// 32 rows go through v_mfma_f32_32x32x16_bf16, whose transposed scores leave
+// half of a row's keys on each of two lanes. Two workgroups share a CU (207 to
+// 228 registers, 68 KB of LDS), one's softmax beside the other's products.
+//
+// Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each
+// 880 TFLOP/s; one prompt of 8192 tokens 965; the largest library product
+// reaches 1520. The matrix cores are busy 48% of the cycles, at a clock that
+// the power limit holds at 1.7 GHz with random data (2.1 with zeros, where the
+// same cycles give 1075): a schedule that keeps them busier runs at a lower
+// clock. Tried, and not faster: the next tile's scores formed beside this
+// tile's softmax (886 against 867), eight waves on 256 rows (+5% for long
+// contexts, -3% for short, and 10% less at heads of 64), the same with its
+// halves taking turns (856), 64 rows per wave (791; half the LDS reads, but
+// one wave per SIMD), forced interleaving of products and softmax (698).
 // ----------------------------------------------------------------------------
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
@@ -804,15 +831,17 @@ struct Grid {
 
 Grid grid_of(const AttnArgs &a) {
     if (a.dtype != SGMV_BF16) return {0, most_groups(a, a.num_requests, kStreamRows) * a.kv_heads + kStreamTarget};
-    // A batch whose requests all fit one row tile of the streaming kernel is its alone.
-    const int64_t one_each = (int64_t)a.num_requests * a.kv_heads + kStreamTarget;
-    if ((int64_t)a.max_q_len * a.group <= kShortRows) return {0, one_each};
+    // A batch whose requests are all short is the streaming kernel's alone.
+    const int64_t rows = (int64_t)a.max_q_len * a.group;
+    const int64_t tiles_each = ((rows < kShortRows ? rows : kShortRows) + kStreamRows - 1) / kStreamRows;
+    const int64_t streams = tiles_each * a.num_requests * a.kv_heads + kStreamTarget;
+    if (rows <= kShortRows) return {0, streams};
     // Otherwise requests go to the two kinds of items by their rows. At most T * group / (kShortRows + 1) are long; a
     // batch of one request has tile items only.
     const int64_t could = (int64_t)a.T * a.group / (kShortRows + 1);
     const bool one = a.num_requests == 1;
     const int64_t longs = one || could >= a.num_requests ? a.num_requests : could;
-    return {most_groups(a, longs, kTileRows) * a.kv_heads + kTileTarget, one ? 0 : one_each};
+    return {most_groups(a, longs, kTileRows) * a.kv_heads + kTileTarget, one ? 0 : streams};
 }
 
 template <typename T>

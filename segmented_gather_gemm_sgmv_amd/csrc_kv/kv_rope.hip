@@ -8,7 +8,12 @@
 //
 // What bounds sgmv_rope_append: HBM. Every q, k and v element is read once
 // and written once (3 flops per element between); a token's table row is read
-// by all of its heads and comes from L2 after the first.
+// by all of its heads and comes from L2 after the first. A workgroup takes 256
+// units of one token (16 bytes of a row or a pair of them), so a decode step
+// of 64 tokens already makes 256 workgroups.
+//
+// Measured: 4583 tokens of 64 + 2 x 8 heads of 128 in bf16, 190 MB, 31.4 us
+// (6.05 TB/s); 64 tokens of 32 + 2 x 32 heads 3.3 us (kernel alone).
 #include "kv_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"

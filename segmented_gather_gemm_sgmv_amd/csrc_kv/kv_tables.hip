@@ -14,7 +14,12 @@
 // requests in its own LDS (a read of 8 bytes per request, from L2 after the
 // first workgroup) and writes its share of the tokens, fresh entries and
 // returned pages, so nothing waits for another workgroup. That is also why
-// the outputs have buffers of their own.
+// the outputs have buffers of their own. The scans run over a wave's lanes by
+// lane shifts, and each thread handles about one token, entry or page.
+//
+// Measured (kernel alone): 64 requests of one token 3.0 us, 512 mixed ones
+// with some 33000 tokens 5.4 us; an empty kernel takes 1.6. With shuffles
+// through LDS and four tokens per thread they took 3.7 and 12.2 us.
 #include "kv_launch.h"
 
 namespace sgmv {

@@ -514,3 +514,45 @@ def test_serving_layer_against_dense(dev, dtype, window):
     worst, seconds = example.serve(layer, 256, 6, 14, 60)
     assert len(seconds) == 14
     assert worst <= (2.0 ** -4 if dtype is BF16 else 8 * 256 * 2.0 ** -24), worst
+
+
+def test_binding_refusals(dev):
+    """What the Python calls refuse before the library is reached."""
+    q = torch.zeros(3, 4, 64, dtype=BF16, device=dev)
+    K = torch.zeros(5, 2, 16, 64, dtype=BF16, device=dev)
+    table, starts, lens = ints(np.zeros((2, 3)), dev), ints([0, 1, 3], dev), ints([1, 2], dev)
+
+    def attend(out=q, q=q, K=K, V=K, table=table, starts=starts, lens=lens, lse=None, ws=None, n=2, scale=0.1):
+        return sg.sgmv_paged_attention(out, q, K, V, table, starts, lens, scale, n, lse=lse, workspace_buf=ws)
+
+    attend(out=torch.empty_like(q))
+    bad = [dict(out=q[:2]), dict(out=q.float()), dict(K=K.float()), dict(V=K[:4]), dict(K=K[..., :32], V=K[..., :32]),
+           dict(table=table[:1]), dict(table=table.long()), dict(starts=starts[:2]), dict(lens=lens.float()),
+           dict(lse=torch.zeros(3, 4, dtype=BF16, device=dev)), dict(lse=torch.zeros(4, 3, device=dev)),
+           dict(q=q.transpose(0, 1)), dict(q=q.cpu()), dict(q=q.half(), out=q.half(), K=K.half(), V=K.half()), dict(q=None)]
+    for b in bad:
+        with pytest.raises((ValueError, TypeError, AttributeError)):
+            attend(**b)
+    for b in (dict(scale=0.0), dict(scale=float("nan")), dict(n=-1), dict(ws=torch.zeros(256, dtype=torch.uint8, device=dev))):
+        with pytest.raises(sg.SGMVError):
+            attend(**b)
+
+    pos, tab = ints([0, 1, 2], dev), torch.zeros(9, 32, 2, device=dev)
+
+    def rope(q_out=q, q=q, k=K[:3, :, 0], v=K[:3, :, 0], K=K, V=K, pos=pos, slot=pos, tab=tab):
+        sg.sgmv_rope_append(q_out, q, k.contiguous() if k is not None else None, v, K, V, pos, slot, tab)
+
+    kv = torch.zeros(3, 2, 64, dtype=BF16, device=dev)
+    for b in [dict(q_out=None), dict(k=kv, v=kv[:2]), dict(k=kv, v=kv.float()), dict(k=kv, v=kv, slot=None),
+              dict(k=kv, v=kv, slot=pos[:2]), dict(k=kv, v=kv, pos=pos[:2]), dict(k=kv, v=kv, tab=tab[..., :1]),
+              dict(k=kv, v=kv, tab=tab.double()), dict(q=None, q_out=None, k=None), dict(k=kv[:, :1], v=kv[:, :1])]:
+        with pytest.raises((ValueError, TypeError)):
+            rope(**b)
+
+    seq = ints([3, 4], dev)
+    with pytest.raises(ValueError):
+        sg.sgmv_kv_tables(seq, ints([1], dev), table, 16, pos, ints([0] * 4, dev), ints([0] * 4, dev), starts, lens, pos, pos)
+    with pytest.raises(ValueError):
+        sg.sgmv_kv_tables(seq, seq, table, 16, pos, ints([0] * 3, dev), ints([0] * 4, dev), starts, lens, pos, pos)
+    with pytest.raises(sg.SGMVError):
+        sg.sgmv_kv_tables(seq, seq, table, 17, pos, ints([0] * 4, dev), ints([0] * 4, dev), starts, lens, pos, pos)
