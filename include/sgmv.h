@@ -504,8 +504,11 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  * left as they were.
  *
  * Products accumulate in fp32 and the softmax's running maximum, sum and
- * output are fp32; with bf16 the weights enter the second product rounded to
- * bf16, and out is rounded once. Results do not depend on timing.
+ * output are fp32; out is rounded once. With bf16 the weights enter the second
+ * product as two bf16 values each (16 significant bits) for requests of at
+ * most 32 new tokens times query heads per cached head, and rounded to bf16
+ * for longer ones (an error of at most 2^-8 sum_j w_j |V_j| / sum_j w_j).
+ * Results do not depend on timing.
  *
  * out          [T][q_heads][head_dim] with its own row stride.
  * lse          device float[T][q_heads], or NULL.

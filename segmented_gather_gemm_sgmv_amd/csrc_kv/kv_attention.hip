@@ -399,11 +399,18 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
             }
 
         if constexpr (S::kBf16) {
-            // Weight slots 8 g + j of this lane: keys 4 g + j (j < 4) and 16 + 4 g + j - 4.
-            const uint4 pw = make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                                        pack_bf16x2(s[NB - 1][0], s[NB - 1][1]),
-                                        pack_bf16x2(s[NB - 1][2], s[NB - 1][3]));
-            const bf16x8_t p = __builtin_bit_cast(bf16x8_t, pw);
+            // Weight slots 8 g + j of this lane: keys 4 g + j (j < 4) and 16 + 4 g + j - 4. A weight enters as two bf16
+            // values, hi = rne(w) and lo = rne(w - hi), 16 significant bits: HBM leaves the time for the second
+            // product, and the result's only rounding that counts is then the one to its own type.
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w0 = s[i / 2][2 * (i % 2)], w1 = s[i / 2][2 * (i % 2) + 1];
+                hi[i] = pack_bf16x2(w0, w1);
+                lo[i] = pack_bf16x2(w0 - __uint_as_float(hi[i] << 16), w1 - __uint_as_float(hi[i] & 0xffff0000u));
+            }
+            const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            const bf16x8_t p_lo = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             const int row = 4 * g + (r >> 2), half = 8 * (r & 1);
 #pragma unroll
             for (int d = 0; d < S::kOut; ++d) {
@@ -414,7 +421,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
                 } vf;
                 vf.h[0] = read_transposed(v_lds + S::v_slot(row, c) * 16 + half);
                 vf.h[1] = read_transposed(v_lds + S::v_slot(row + 16, c) * 16 + half);
-                o[d] = mfma16(vf.v, p, o[d]);
+                o[d] = mfma16(vf.v, p_lo, mfma16(vf.v, p, o[d]));
             }
         } else {
 #pragma unroll
