@@ -499,9 +499,9 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  * a sliding window, with the first `sinks` tokens always visible.
  *     out = sum_j w_j V_j / sum_j w_j,   w_j = exp(scale * q . K_j)
  *     lse = log(sum_j w_j)
- * A row that sees no key gets out = 0 and lse = -infinity. Keys that no row
- * of a request sees are not used, whatever they hold. Rows of no request are
- * left as they were.
+ * A row that sees no key gets out = 0 and lse = -infinity. A key that a row
+ * does not see changes nothing of that row, whatever it holds. Rows of no
+ * request are left as they were.
  *
  * Products accumulate in fp32 and the softmax's running maximum, sum and
  * output are fp32; out is rounded once. With bf16 the weights enter the second

@@ -62,6 +62,7 @@ struct StreamSmem {
     float m[kWaves][16], l[kWaves][16];  // the waves' running maxima and sums
     float part[2][kThreads];             // add_splits
     int flag;
+    int odd;  // the tile kernel cleared values that are not finite
 };
 
 // D: columns of a row in LDS; U: columns that products run over, at least
@@ -121,6 +122,54 @@ typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 // rows.
 __device__ __forceinline__ s16x4_t read_transposed(const void *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)p);
+}
+
+// Values that are not finite. In a tile that some rows see and others do not they would reach all rows, since a zero
+// weight does not take a NaN or an infinity out of a product: they enter it as 0, and are given to the rows that see
+// them afterwards (any positive weight leaves such a value what it is). Measured: the check of the tiles on the mask's
+// edge costs chunks 0 to 3%, and the test at a sum's end 0.2 us of a decode step (one request of 2000 keys: 11.3 -> 11.7 us).
+template <typename T>
+__device__ __forceinline__ bool is_finite(T x) {
+    if constexpr (sizeof(T) == 2)
+        return (x.bits & 0x7f80u) != 0x7f80u;
+    else
+        return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+}
+
+// Replaces them in a run of 16 bytes by 0; returns whether there were any.
+template <typename T>
+__device__ __forceinline__ bool clear_nonfinite(uint4 &v) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t keep = 0;
+        if constexpr (sizeof(T) == 2) {
+            keep |= (w[i] & 0x7f80u) != 0x7f80u ? 0xffffu : 0u;
+            keep |= (w[i] & 0x7f800000u) != 0x7f800000u ? 0xffff0000u : 0u;
+        } else {
+            keep = (w[i] & 0x7f800000u) != 0x7f800000u ? ~0u : 0u;
+        }
+        any |= keep != ~0u;
+        w[i] &= keep;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+    return any;
+}
+
+// Element `col` of the cached value of a key that a row sees, or 0 where it is finite.
+template <typename T>
+__device__ __forceinline__ float nonfinite_value(const AttnArgs &a, const Item &it, int key, int col) {
+    const int at = key >> a.page_shift;
+    const int p = a.block_table[(int64_t)it.b * a.max_blocks + at];
+    const int page = (unsigned)p < (unsigned)a.num_pages ? p : 0;
+    const int64_t row = (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+    const T x = static_cast<const T *>(a.V)[row * a.head_dim + col];
+    if (is_finite(x)) return 0.f;
+    if constexpr (sizeof(T) == 2)
+        return __uint_as_float((uint32_t)x.bits << 16);
+    else
+        return x;
 }
 
 // Writes one row's result: sum / weight, rounded once, and the log-sum-exp.
@@ -323,6 +372,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 #pragma unroll
     for (int d = 0; d < S::kOut; ++d) o[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+    bool odd = false;  // values that are not finite, in a tile that not every row sees all of
     load_pages(0);
     if (first < t1) load_tile(0, first);
     for (int i = 0, v = first; v < t1; ++i, v += kWaves) {
@@ -335,8 +385,12 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
             for (int j = 0; j < NL; ++j) {
                 const int f = j * 64 + lane, row = 16 * nb + f / CH, c = f % CH, key = key0 + row;
                 uint4 vv = vr[nb * NL + j];
-                // Values of keys that no row sees meet zero weights, which a NaN would survive.
-                if (!whole && (key > pb || (key < pa_lo && key >= a.sinks))) vv = make_uint4(0, 0, 0, 0);
+                if (!whole) {
+                    if (key > pb || (key < pa_lo && key >= a.sinks))
+                        vv = make_uint4(0, 0, 0, 0);  // no row sees it
+                    else if (pa != pb)  // rows of one token see the same keys
+                        odd |= clear_nonfinite<T>(vv);
+                }
                 if (c < nch) {
                     reinterpret_cast<uint4 *>(k_lds)[S::k_slot(row, c)] = kr[nb * NL + j];
                     reinterpret_cast<uint4 *>(v_lds)[S::v_slot(row, c)] = vv;
@@ -434,9 +488,37 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
         }
         wave_lds_order();
     }
+    l = swap32_sum(swap16_sum(l));
+    // A sum over a value that is not finite is that value, which was cleared, or met a weight's zero low part.
+#pragma unroll
+    for (int d = 0; d < S::kOut; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd |= o[d][e] != o[d][e] && l == l;
+    if (__any(odd)) {
+        f32x4_t x[S::kOut];
+#pragma unroll
+        for (int d = 0; d < S::kOut; ++d) x[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int v = first; v < t1; v += kWaves) {
+            const int key0 = run.tile(v) * S::kKeys;
+            for (int key = key0; key < key0 + S::kKeys; ++key) {
+                const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+                if (!__any(seen)) continue;
+#pragma unroll
+                for (int d = 0; d < S::kOut; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int col = 16 * d + 4 * g + e;
+                        if (seen && col < a.head_dim) x[d][e] += nonfinite_value<T>(a, it, key, col);
+                    }
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < S::kOut; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = x[d][e] != 0.f ? x[d][e] : o[d][e];
+    }
 
     // The four waves' results meet in LDS, in wave order.
-    l = swap32_sum(swap16_sum(l));
     if (g == 0) {
         sm.m[wave][r] = m;
         sm.l[wave][r] = l;
@@ -585,7 +667,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     const int q_head = it.head * a.group + my % a.group;
     const int pos = valid ? it.p0 + tok : -1;
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
-    const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0;
+    const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
     const int head_dim = kFull ? D : a.head_dim, nch = head_dim / 8;
     bf16x8_t qf[L::kSteps];
@@ -659,19 +741,25 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
                   8 * (lane & 1);
 
     const int n = t1 - t0;
+    const auto all_see = [&](int key0) {  // every row sees every key of the tile
+        return key0 + kTileKeys - 1 <= pa && (pb_lo <= key0 || key0 + kTileKeys <= a.sinks);
+    };
     auto step = [&](int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
         if (i + 1 < n) {
             if ((i + 1) % 16 == 0) load_pages(i + 1);
             load_tile(i + 1, k_next, v_next);
         }
         const int key0 = run.tile(t0 + i) * kTileKeys;
-        if (!(key0 + kTileKeys - 1 <= pb && (pa_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
-            // Values of keys that no row sees meet zero weights, which a NaN would survive.
+        if (!all_see(key0)) {
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
                 const int f = j * kThreads + tid, key = key0 + f / CH;
-                if (key > pb || (key < pa_lo && key >= a.sinks))
-                    reinterpret_cast<uint4 *>(vb)[f] = make_uint4(0, 0, 0, 0);
+                uint4 v = reinterpret_cast<uint4 *>(vb)[f];
+                const bool unseen = key > pb || (key < pa_lo && key >= a.sinks);  // by every row
+                if (unseen) v = make_uint4(0, 0, 0, 0);
+                const bool cleared = clear_nonfinite<bf16_t>(v);
+                if (unseen || cleared) reinterpret_cast<uint4 *>(vb)[f] = v;
+                if (cleared) sm.odd = 1;
             }
             lds_barrier();
         }
@@ -742,6 +830,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
         }
         loads_barrier();
     };
+    if (tid == 0) sm.odd = 0;
     if (n > 0) {
         load_pages(0);
         load_tile(0, k_even, v_even);
@@ -750,6 +839,24 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     for (int i = 0; i < n; i += 2) {
         step(i, k_even, v_even, k_odd, v_odd);
         if (i + 1 < n) step(i + 1, k_odd, v_odd, k_even, v_even);
+    }
+    if (sm.odd) {
+        for (int i = 0; i < n; ++i) {
+            const int key0 = run.tile(t0 + i) * kTileKeys;
+            if (all_see(key0)) continue;
+            for (int key = key0; key < key0 + kTileKeys; ++key) {
+                const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
+                if (!__any(seen)) continue;
+#pragma unroll
+                for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int col = 32 * d + 8 * (e / 4) + 4 * h + e % 4;
+                        if (seen && col < head_dim) o[d][e] += nonfinite_value<bf16_t>(a, it, key, col);
+                        __builtin_amdgcn_sched_barrier(0);  // one at a time: rare, and no registers for more
+                    }
+            }
+        }
     }
 
     l = swap32_sum(l);

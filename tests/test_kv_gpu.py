@@ -390,6 +390,45 @@ def test_infinite_and_nan_inputs_stay_in_their_rows(dev, dtype):
     assert torch.equal(out3[keep], out[keep]) and torch.equal(lse3[keep], lse[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,ctx,hq,hk,D,window,sinks", [
+    ([7, 1], [90, 40], 4, 2, 64, 0, 0),        # streamed in both types
+    ([15, 2], [100, 30], 2, 1, 128, 20, 3),
+    ([40, 1], [70, 90], 6, 2, 80, 0, 0),       # several row tiles, a narrower head
+    ([150, 33], [20, 300], 8, 2, 128, 64, 5),
+    ([200], [100], 1, 1, 64, 33, 70),
+    ([1, 1], [400, 31], 8, 1, 128, 0, 0),      # single tokens: a value's infinity stays one
+])
+def test_values_that_are_not_finite_reach_only_the_rows_that_see_them(dev, dtype, new, ctx, hq, hk, D, window, sinks):
+    """Causal masks and windows hide a key from some rows of a request and not
+    from others; a NaN or an infinity in one column of its value belongs to the
+    others' same column alone."""
+    rng = np.random.default_rng(sum(new) + D)
+    q, K, V, table, q_start, kv = paged(rng, dev, new, ctx, hq, hk, D, dtype, 16)
+    clean, odd = f64(V), V.clone()
+    want = np.zeros(q.shape)   # what each element gets from values that are not finite
+    for b in range(len(new)):
+        p = np.arange(ctx[b], kv[b])
+        keys = {int(kv[b]) - 1, int(kv[b]) - 2, ctx[b], ctx[b] + new[b] // 2, max(ctx[b] - 7, 0), 1}
+        for n, j in enumerate(sorted(keys)):
+            x = [float("nan"), float("inf"), float("-inf")][n % 3]
+            head, cols = n % hk, [(11 * n) % D, D - 1 - n]
+            seen = (j <= p) & ((j > p - window) | (j < sinks) | (window == 0))
+            for c in cols:
+                odd[table[b, j // 16], head, j % 16, c] = x
+                clean[table[b, j // 16], head, j % 16, c] = 0.0
+                for h in range(head * (hq // hk), (head + 1) * (hq // hk)):
+                    want[q_start[b]:q_start[b + 1], h, c] += np.where(seen, x, 0.0)
+    out, lse = attend(dev, q, K, odd, table, q_start, kv, window, sinks)
+    o, l, to, tl = ref.attend(f64(q), f64(K), clean, table, q_start, kv, D ** -0.5, window, sinks, dtype is BF16)
+    spoilt, got = ~np.isfinite(want), f64(out)
+    assert spoilt.any() and not spoilt.all()
+    assert np.array_equal(got[spoilt], want[spoilt], equal_nan=True)
+    got[spoilt] = o[spoilt]
+    within(torch.tensor(got), o, to, "out")
+    within(lse, l, tl, "lse")
+
+
 def test_same_bits_twice_without_lse_and_on_another_stream(dev):
     rng = np.random.default_rng(6)
     for new, ctx in (([1] * 3, [5000, 900, 40]), ([100, 1], [3000, 2500])):
