@@ -507,7 +507,8 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  * output are fp32; out is rounded once. With bf16 the weights enter the second
  * product as two bf16 values each (16 significant bits) for requests of at
  * most 32 new tokens times query heads per cached head, and rounded to bf16
- * for longer ones (an error of at most 2^-8 sum_j w_j |V_j| / sum_j w_j).
+ * for longer ones (an error of at most 2^-8 sum_j w_j |V_j| / sum_j w_j); a
+ * call for one request goes by max_q_len instead of its tokens.
  * Results do not depend on timing.
  *
  * out          [T][q_heads][head_dim] with its own row stride.
@@ -516,6 +517,7 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  * max_q_len    at least the largest number of new tokens of a request (the
  *              first max_q_len of more are computed).
  * scale        positive and finite. window, sinks: >= 0.
+ * max_blocks   max_blocks * page_size at most 2^30.
  * workspace    as sgmv_paged_attention_workspace_bytes says for the same
  *              sizes, 256-byte aligned, zero-filled before its first use; its
  *              counters are zero again after every call. Not to be shared

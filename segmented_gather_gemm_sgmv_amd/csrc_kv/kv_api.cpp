@@ -147,7 +147,9 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
     if (((rows / 16 + 1) * kv_heads + sgmv::kMostSplits) * num_requests > INT32_MAX) return SGMV_ERR_SHAPE;
     int st = check_pages(num_pages, page_size);
     if (st != SGMV_OK) return st;
-    if ((int64_t)max_blocks * page_size > INT32_MAX) return SGMV_ERR_SHAPE;
+    // positions, and the ends of key tiles past them, in 31 bits; and a window past the longest context changes nothing
+    const int far = 1 << 30;
+    if ((int64_t)max_blocks * page_size > far) return SGMV_ERR_SHAPE;
     if (!(scale > 0.f) || !isfinite(scale)) return SGMV_ERR_SHAPE;
     if (T == 0 || num_requests == 0 || max_q_len == 0) return SGMV_OK;
     if (!out || !q || !K_cache || !V_cache || !q_start || !kv_len || (max_blocks > 0 && !block_table))
@@ -159,8 +161,6 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         workspace_bytes < sgmv::attention_workspace_bytes(head_dim, dtype))
         return SGMV_ERR_WORKSPACE;
-    // A window past the longest context, and sinks past it, change nothing.
-    const int far = 1 << 30;
     const sgmv::AttnArgs a{out,       out_stride,   lse,         q,        q_stride,
                            q_heads,   q_heads / kv_heads, K_cache, V_cache, num_pages,
                            kv_heads,  page_shift(page_size), head_dim, block_table, max_blocks,

@@ -91,6 +91,12 @@ def test_attention_refusals():
         assert attention(**none, q=None, out=None, ws=None) == 0, none
 
 
+def test_attention_positions_stay_in_31_bits():
+    """The end of the key tile past the last position has to be an int too."""
+    assert attention(width=(1 << 26) + 1) == SHAPE
+    assert attention(width=1 << 26, T=0) == 0
+
+
 def test_attention_workspace_bytes():
     f = sg.lib.sgmv_paged_attention_workspace_bytes
     assert f(12, 1) == 0 and f(136, 1) == 0 and f(0, 1) == 0 and f(64, 2) == 0
