@@ -622,6 +622,14 @@ class PagedKVCache:
         self._pool[0][1] = num_pages
         self.q_start = ints(max_requests + 1)
         self.position = self.slot = ints(0)
+        self._slot_stream = _stream(self.slot, None)
+
+    def _use_slots(self, stream) -> None:
+        """Keeps position and slot, which a later step may replace, until `stream`'s work on them is done."""
+        if _stream(self.slot, stream) != self._slot_stream:
+            s = _torch_stream(self.slot.device, stream)
+            self.position.record_stream(s)
+            self.slot.record_stream(s)
 
     @property
     def kv_len(self) -> torch.Tensor:
@@ -640,6 +648,8 @@ class PagedKVCache:
             with torch.cuda.stream(_torch_stream(self.slot.device, stream)):
                 self.position = torch.empty(num_tokens, dtype=torch.int32, device=self.slot.device)
                 self.slot = torch.empty_like(self.position)
+            self._slot_stream = _stream(self.slot, stream)
+        self._use_slots(stream)
         sgmv_kv_tables(self._len[0], new_len, self.block_table, self.page_size, self.free_pages, self._pool[0],
                        self._pool[1], self.q_start, self._len[1], self.position, self.slot, stream)
         self._len.reverse()
@@ -648,6 +658,7 @@ class PagedKVCache:
     def append(self, q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                table: Optional[torch.Tensor], interleaved: bool = False, layer: int = 0, stream=None) -> None:
         """q_out = q rotated; k (rotated) and v of the step's tokens to the cache."""
+        self._use_slots(stream)
         sgmv_rope_append(q_out, q, k, v, self.K[layer], self.V[layer], self.position, self.slot, table, interleaved,
                          stream)
 

@@ -555,6 +555,24 @@ def test_serving_layer_against_dense(dev, dtype, window):
     assert worst <= (2.0 ** -4 if dtype is BF16 else 8 * 256 * 2.0 ** -24), worst
 
 
+def test_slots_are_kept_for_another_stream(dev):
+    """A step of another size replaces position and slot; a stream that still
+    reads the old ones keeps their memory."""
+    cache = sg.PagedKVCache(8, 16, 1, 64, 2, 4, dtype=F32, device=dev)
+    x = torch.ones(5, 1, 64, device=dev)
+    cache.step(ints([3, 2], dev), 5)
+    old = {cache.position.data_ptr(), cache.slot.data_ptr()}
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)   # tens of milliseconds
+        cache.append(torch.empty_like(x), x, x, x, None)
+    cache.step(ints([1, 1], dev), 2)
+    assert not old & {cache.position.data_ptr(), cache.slot.data_ptr()}
+    torch.cuda.synchronize()
+    assert float(cache.K.sum()) == 5 * 64 and float(cache.V.sum()) == 5 * 64
+
+
 def test_binding_refusals(dev):
     """What the Python calls refuse before the library is reached."""
     q = torch.zeros(3, 4, 64, dtype=BF16, device=dev)
