@@ -37,7 +37,7 @@ constexpr float kSlack = 8.f;
 // Two workgroups fit a CU; their eight waves keep 128 KB in flight.
 //
 // Measured, bf16, heads of 128: 512 requests of 128 to 4096 keys, 64 heads on
-// 8, 716 us (6.4 TB/s); 64 requests of 1 to 2048 keys, 32 heads, 161 us
+// 8, 721 us (6.3 TB/s); 64 requests of 1 to 2048 keys, 32 heads, 162 us
 // (6.2 TB/s); one request of 131001 keys, 64 heads on 8, 64 splits a head,
 // 92 us (5.8 TB/s); a plain streaming read reaches 5.5 to 5.9 TB/s without
 // the streaming hint. Where there is too little work to fill the GPU a wave's
@@ -576,12 +576,12 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 // 64 that its waves share: the next tile is loaded straight to the other of
 // two LDS buffers while the present one is worked on, one barrier per tile.
 // 32 rows go through v_mfma_f32_32x32x16_bf16, whose transposed scores leave
-// half of a row's keys on each of two lanes. Two workgroups share a CU (207 to
+// half of a row's keys on each of two lanes. Two workgroups share a CU (up to
 // 228 registers, 68 KB of LDS), one's softmax beside the other's products.
 //
 // Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each
-// 880 TFLOP/s; one prompt of 8192 tokens 965; the largest library product
-// reaches 1520. The matrix cores are busy 48% of the cycles, at a clock that
+// 830 to 880 TFLOP/s by card; one prompt of 8192 tokens 900 to 950; the largest
+// library product reaches 1520. The matrix cores are busy 48% of the cycles, at a clock that
 // the power limit holds at 1.7 GHz with random data (2.1 with zeros, where the
 // same cycles give 1075): a schedule that keeps them busier runs at a lower
 // clock. Tried, and not faster: the next tile's scores formed beside this
