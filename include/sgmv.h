@@ -505,10 +505,7 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  *
  * Products accumulate in fp32 and the softmax's running maximum, sum and
  * output are fp32; out is rounded once. With bf16 the weights enter the second
- * product as two bf16 values each (16 significant bits) for requests of at
- * most 32 new tokens times query heads per cached head, and rounded to bf16
- * for longer ones (an error of at most 2^-8 sum_j w_j |V_j| / sum_j w_j); a
- * call for one request goes by max_q_len instead of its tokens.
+ * product as two bf16 values each (16 significant bits).
  * Results do not depend on timing.
  *
  * out          [T][q_heads][head_dim] with its own row stride.

@@ -157,19 +157,52 @@ __device__ __forceinline__ bool clear_nonfinite(uint4 &v) {
     return any;
 }
 
-// Element `col` of the cached value of a key that a row sees, or 0 where it is finite.
+// Columns col .. col + 3 of a key's value, 0 where they are finite.
 template <typename T>
-__device__ __forceinline__ float nonfinite_value(const AttnArgs &a, const Item &it, int key, int col) {
-    const int at = key >> a.page_shift;
-    const int p = a.block_table[(int64_t)it.b * a.max_blocks + at];
-    const int page = (unsigned)p < (unsigned)a.num_pages ? p : 0;
-    const int64_t row = (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-    const T x = static_cast<const T *>(a.V)[row * a.head_dim + col];
-    if (is_finite(x)) return 0.f;
-    if constexpr (sizeof(T) == 2)
-        return __uint_as_float((uint32_t)x.bits << 16);
-    else
-        return x;
+__device__ __forceinline__ f32x4_t nonfinite4(const T *value, int col) {
+    f32x4_t x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const T v = value[col + e];
+        if constexpr (sizeof(T) == 2)
+            x[e] = is_finite(v) ? 0.f : __uint_as_float((uint32_t)v.bits << 16);
+        else
+            x[e] = is_finite(v) ? 0.f : v;
+    }
+    return x;
+}
+
+// Calls add(key, the key's value) for the keys of tiles v0, v0 + step, ... below v1 that lie in a 16-key block with
+// values that are not finite. The wave looks for them 16 bytes per lane, so that a long context costs a read of its
+// values and not a visit of every key.
+template <typename T, int kKeys, typename Add>
+__device__ __forceinline__ void each_nonfinite(const AttnArgs &a, const Item &it, const TileRun &run, int v0, int v1, int step,
+                                               Add add) {
+    for (int v = v0; v < v1; v += step) {
+        const int first = run.tile(v) * kKeys;
+        for (int key0 = first; key0 < first + kKeys; key0 += 16) {
+            const int at = key0 >> a.page_shift;
+            if (at >= a.max_blocks) break;  // past the request's last key
+            const int p = a.block_table[(int64_t)it.b * a.max_blocks + at];
+            const int page = (unsigned)p < (unsigned)a.num_pages ? p : 0;
+            const int64_t row = (((int64_t)page * a.kv_heads + it.head) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
+            const T *values = static_cast<const T *>(a.V) + row * a.head_dim;
+            bool odd = false;
+            for (int f = threadIdx.x & 63; f < 16 * a.head_dim / Elem<T>::kPerVec; f += 64) {
+                uint4 x = ld16(values + f * Elem<T>::kPerVec);
+                odd |= clear_nonfinite<T>(x);
+            }
+            if (!__any(odd)) continue;
+            for (int k = 0; k < 16; ++k) add(key0 + k, values + k * a.head_dim);
+        }
+    }
+}
+
+// Two weights as two bf16 values each, hi = rne(w) and lo = rne(w - hi): 16 significant bits, so that the result's only
+// rounding that counts is the one to its own type. (Rounded once they would double the result's squared error.)
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(w0, w1);
+    lo = pack_bf16x2(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xffff0000u));
 }
 
 // Writes one row's result: sum / weight, rounded once, and the log-sum-exp.
@@ -453,16 +486,11 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
             }
 
         if constexpr (S::kBf16) {
-            // Weight slots 8 g + j of this lane: keys 4 g + j (j < 4) and 16 + 4 g + j - 4. A weight enters as two bf16
-            // values, hi = rne(w) and lo = rne(w - hi), 16 significant bits: HBM leaves the time for the second
-            // product, and the result's only rounding that counts is then the one to its own type.
+            // Weight slots 8 g + j of this lane: keys 4 g + j (j < 4) and 16 + 4 g + j - 4. HBM leaves the time for the
+            // second product.
             uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w0 = s[i / 2][2 * (i % 2)], w1 = s[i / 2][2 * (i % 2) + 1];
-                hi[i] = pack_bf16x2(w0, w1);
-                lo[i] = pack_bf16x2(w0 - __uint_as_float(hi[i] << 16), w1 - __uint_as_float(hi[i] & 0xffff0000u));
-            }
+            for (int i = 0; i < 4; ++i) split_weights(s[i / 2][2 * (i % 2)], s[i / 2][2 * (i % 2) + 1], hi[i], lo[i]);
             const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
             const bf16x8_t p_lo = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             const int row = 4 * g + (r >> 2), half = 8 * (r & 1);
@@ -498,20 +526,15 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
         f32x4_t x[S::kOut];
 #pragma unroll
         for (int d = 0; d < S::kOut; ++d) x[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        for (int v = first; v < t1; v += kWaves) {
-            const int key0 = run.tile(v) * S::kKeys;
-            for (int key = key0; key < key0 + S::kKeys; ++key) {
-                const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
-                if (!__any(seen)) continue;
+        each_nonfinite<T, S::kKeys>(a, it, run, first, t1, kWaves, [&](int key, const T *value) {
+            const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+            if (!__any(seen)) return;
 #pragma unroll
-                for (int d = 0; d < S::kOut; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int col = 16 * d + 4 * g + e;
-                        if (seen && col < a.head_dim) x[d][e] += nonfinite_value<T>(a, it, key, col);
-                    }
+            for (int d = 0; d < S::kOut; ++d) {
+                const int col = 16 * d + 4 * g;
+                if (seen && col < a.head_dim) x[d] += nonfinite4(value, col);
             }
-        }
+        });
 #pragma unroll
         for (int d = 0; d < S::kOut; ++d)
 #pragma unroll
@@ -578,17 +601,21 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 // 32 rows go through v_mfma_f32_32x32x16_bf16, whose transposed scores leave
 // half of a row's keys on each of two lanes. Two workgroups share a CU (up to
 // 228 registers, 68 KB of LDS), one's softmax beside the other's products.
+// The weights enter the second product as two bf16 values, as in the streaming
+// kernel, so a request's precision does not depend on its length; the flops
+// below count the products that the operator has, not this third one.
 //
-// Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each
-// 830 to 880 TFLOP/s by card; one prompt of 8192 tokens 900 to 950; the largest
-// library product reaches 1520. The matrix cores are busy 48% of the cycles, at a clock that
-// the power limit holds at 1.7 GHz with random data (2.1 with zeros, where the
-// same cycles give 1075): a schedule that keeps them busier runs at a lower
-// clock. Tried, and not faster: the next tile's scores formed beside this
-// tile's softmax (886 against 867), eight waves on 256 rows (+5% for long
-// contexts, -3% for short, and 10% less at heads of 64), the same with its
-// halves taking turns (856), 64 rows per wave (791; half the LDS reads, but
-// one wave per SIMD), forced interleaving of products and softmax (698).
+// Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each 690
+// TFLOP/s, one prompt of 8192 tokens 740; the largest library product reaches
+// 1520. With weights of 8 bits these were 870 and 960, and the result's error
+// against 64 bits 1.4 times as large (2.3e-3 of its norm, against 1.66e-3).
+// In that form the matrix cores were busy 48% of the cycles, at 1.7 GHz with
+// random data and 2.1 with zeros, and these schedules were tried: the next
+// tile's scores formed beside this tile's softmax (886 against 867), eight
+// waves on 256 rows (+5% for long contexts, -3% for short, and 10% less at
+// heads of 64), the same with its halves taking turns (856), 64 rows per wave
+// (791; half the LDS reads, but one wave per SIMD), forced interleaving of
+// products and softmax (698).
 // ----------------------------------------------------------------------------
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
@@ -681,7 +708,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             qf[k] = __builtin_bit_cast(bf16x8_t, valid && c < nch ? v : make_uint4(0, 0, 0, 0));
         }
     }
-    if (!kFull) {  // the chunks past the head stay zero: the chunks past it stay zero
+    if (!kFull) {  // the chunks past the head stay zero
         for (int i = tid; i < L::kBytes / 16; i += kThreads)
             for (unsigned char *buf : {k_even, v_even, k_odd, v_odd})
                 reinterpret_cast<uint4 *>(buf)[i] = make_uint4(0, 0, 0, 0);
@@ -816,9 +843,11 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
                     w[e] = exp2_fast(__builtin_fmaf(s[t / 2][t % 2 * 8 + e], c2, -ref));
                     l += w[e];
                 }
-                const bf16x8_t p = __builtin_bit_cast(
-                    bf16x8_t, make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]),
-                                         pack_bf16x2(w[6], w[7])));
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split_weights(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
+                const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                const bf16x8_t p_lo = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                 if (t < 3) {
 #pragma unroll
                     for (int d = 0; d < L::kOut; ++d)
@@ -826,6 +855,8 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
                 }
 #pragma unroll
                 for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p, o[d]);
+#pragma unroll
+                for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p_lo, o[d]);
             }
         }
         loads_barrier();
@@ -840,26 +871,40 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
         step(i, k_even, v_even, k_odd, v_odd);
         if (i + 1 < n) step(i + 1, k_odd, v_odd, k_even, v_even);
     }
-    if (sm.odd) {
-        for (int i = 0; i < n; ++i) {
-            const int key0 = run.tile(t0 + i) * kTileKeys;
-            if (all_see(key0)) continue;
-            for (int key = key0; key < key0 + kTileKeys; ++key) {
-                const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
-                if (!__any(seen)) continue;
+    l = swap32_sum(l);
+    // A sum over a value that is not finite is that value, which was cleared, or met a weight's zero low part.
+    bool odd = sm.odd != 0;
 #pragma unroll
-                for (int d = 0; d < L::kOut; ++d)
+    for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int col = 32 * d + 8 * (e / 4) + 4 * h + e % 4;
-                        if (seen && col < head_dim) o[d][e] += nonfinite_value<bf16_t>(a, it, key, col);
-                        __builtin_amdgcn_sched_barrier(0);  // one at a time: rare, and no registers for more
-                    }
-            }
-        }
+        for (int e = 0; e < 16; ++e) odd |= o[d][e] != o[d][e];
+    if (__any(odd && valid && l == l)) {
+        f32x16_t x[L::kOut];
+#pragma unroll
+        for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[d][e] = 0.f;
+        each_nonfinite<bf16_t, kTileKeys>(a, it, run, t0, t1, 1, [&](int key, const bf16_t *value) {
+            const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
+            if (!__any(seen)) return;
+#pragma unroll
+            for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const int col = 32 * d + 2 * e + 4 * h;
+                    f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+                    if (seen && col < head_dim) y = nonfinite4(value, col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[d][e + i] += y[i];
+                    __builtin_amdgcn_sched_barrier(0);  // a few at a time: rare, and no registers for more
+                }
+        });
+#pragma unroll
+        for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] = x[d][e] != 0.f ? x[d][e] : o[d][e];
     }
 
-    l = swap32_sum(l);
     const __amdgpu_buffer_rsrc_t part =
         part_rsrc(slots + (int64_t)it.first_slot * L::kSlotFloats, (uint32_t)splits * L::kSlotFloats * 4);
     if (valid) {
