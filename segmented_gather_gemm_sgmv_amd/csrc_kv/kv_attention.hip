@@ -468,8 +468,9 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, s[nb][e]);
         top = swap32_max(swap16_max(top)) * c2;
-        if (__any(top > m + kSlack || (m == kNone && top > kNone))) {
-            const float to = fmaxf(m, top);
+        const bool move = top > m + kSlack;  // of this row: the others keep their reference points, and so their bits
+        if (__any(move)) {
+            const float to = move ? top : m;
             const float keep = exp2_fast(m - ref_of(to));
             l *= keep;
 #pragma unroll
@@ -826,8 +827,9 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
             top = swap32_max(top) * c2;
-            if (__any(top > m + kSlack)) {
-                const float to = fmaxf(m, top);
+            const bool move = top > m + kSlack;  // of this row, as above
+            if (__any(move)) {
+                const float to = move ? top : m;
                 const float keep = exp2_fast(m - ref_of(to));
                 l *= keep;
 #pragma unroll

@@ -49,3 +49,29 @@ def test_weights_hold_16_bits(dev, dtype, new, ctx, hq, hk, D):  # noqa: F811
         tol = tol - 1.01 * (ref.U16 - 2.0 ** -16)
     assert tol.max() < 4e-4
     within(out, o, tol, "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new,ctx,hq,hk,D", [([15], [420], 4, 2, 64), ([8, 7], [500, 410], 12, 3, 128),  # streamed in both types
+                                             ([60], [400], 4, 2, 64), ([150, 70], [330, 700], 8, 4, 128)])
+def test_a_row_is_its_own(dev, dtype, new, ctx, hq, hk, D):  # noqa: F811
+    """The last token's key, whatever it holds, leaves the bits of the tokens
+    before it as they are. Scores grow along the context (by less than the
+    slack within which a reference point may stay), so rows that followed
+    another row's change of reference point would be rounded differently."""
+    rng = np.random.default_rng(D + len(new))
+    q, K, V, table, q_start, kv = paged(rng, dev, new, ctx, hq, hk, D, dtype, 16)
+    last = [(table[b, (kv[b] - 1) // 16], (kv[b] - 1) % 16) for b in range(len(new))]
+    for b in range(len(new)):
+        for j in range(kv[b]):
+            K[table[b, j // 16], :, j % 16] *= 0.3 + j / kv[b]
+    before = np.concatenate([np.arange(q_start[b], q_start[b + 1] - 1) for b in range(len(new))])
+    out, lse = attend(dev, q, K, V, table, q_start, kv)
+    for factor in (60.0, -60.0, 1e4):
+        K2 = K.clone()
+        for page, at in last:
+            K2[page, :, at] *= factor
+        out2, lse2 = attend(dev, q, K2, V, table, q_start, kv)
+        assert not torch.equal(lse, lse2)
+        assert torch.equal(lse[before], lse2[before]), factor
+        assert torch.equal(out[before], out2[before]), factor
