@@ -516,10 +516,14 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
  * scale        positive and finite. window, sinks: >= 0.
  * max_blocks   max_blocks * page_size at most 2^30.
  * workspace    as sgmv_paged_attention_workspace_bytes says for the same
- *              sizes, 256-byte aligned, zero-filled before its first use; its
- *              counters are zero again after every call. Not to be shared
- *              with the calls above or between calls that overlap in time.
+ *              sizes, 256-byte aligned. Its first SGMV_ATTENTION_COUNTER_BYTES
+ *              are counters: zero before its first use, and zero again after
+ *              every call. Not to be shared with the calls above or between
+ *              calls that overlap in time, replays of a captured call among
+ *              them.
  */
+#define SGMV_ATTENTION_COUNTER_BYTES 8192
+
 int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t q_stride,
                          int32_t q_heads, const void *K_cache, const void *V_cache, int32_t num_pages,
                          int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *block_table,

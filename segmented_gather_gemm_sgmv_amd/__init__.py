@@ -117,6 +117,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None, dim=None) -> int:
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a stream object
+_current_is_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _stream(t: torch.Tensor, stream) -> int:
@@ -125,6 +126,10 @@ def _stream(t: torch.Tensor, stream) -> int:
         if index < 0:
             raise ValueError("every tensor must be on a GPU device")
         return _raw_stream(index)
+    return _stream_handle(stream)
+
+
+def _stream_handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -553,24 +558,43 @@ def sgmv_rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k
         raise SGMVError("sgmv_rope_append", st)
 
 
+SGMV_ATTENTION_COUNTER_BYTES = 8192
 _attention_workspaces: Dict[tuple, torch.Tensor] = {}
 
 
+def _capturing(index: int, stream) -> bool:
+    """Whether `stream` (None: device `index`'s current one) is being captured into a graph."""
+    if index == torch.cuda.current_device() and (stream is None or _stream_handle(stream) == _raw_stream(index)):
+        return _current_is_capturing()
+    with torch.cuda.device(index), torch.cuda.stream(_torch_stream(torch.device("cuda", index), stream)):
+        return _current_is_capturing()
+
+
+def _new_attention_workspace(index: int, head_dim: int, dtype: torch.dtype, stream) -> torch.Tensor:
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    nbytes = int(lib.sgmv_paged_attention_workspace_bytes(head_dim, _DTYPES[dtype]))
+    with torch.cuda.device(index), torch.cuda.stream(_torch_stream(torch.device("cuda", index), stream)):
+        ws = torch.empty(max(nbytes, SGMV_ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=f"cuda:{index}")
+        ws[:SGMV_ATTENTION_COUNTER_BYTES].zero_()
+    return ws
+
+
 def attention_workspace(device: torch.device, head_dim: int, dtype: torch.dtype, stream=None) -> torch.Tensor:
-    """A zero-filled workspace for sgmv_paged_attention, cached per (device,
-    stream, dtype, head width). It is not the SGMV calls' workspace."""
+    """A workspace for sgmv_paged_attention with its counters cleared, cached
+    per (device, stream, dtype, head width). It is not the SGMV calls'
+    workspace. Not made while its stream is being captured into a graph: the
+    clearing would then be a node of that graph, not done, and the memory the
+    graph's."""
     device = torch.device(device)
     index = torch.cuda.current_device() if device.index is None else device.index
     handle = _raw_stream(index) if stream is None else _torch_stream(device, stream).cuda_stream
     key = (index, handle, dtype, head_dim)
     ws = _attention_workspaces.get(key)
     if ws is None:
-        if dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
-        nbytes = int(lib.sgmv_paged_attention_workspace_bytes(head_dim, _DTYPES[dtype]))
-        with torch.cuda.device(index), torch.cuda.stream(_torch_stream(torch.device("cuda", index), stream)):
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=f"cuda:{index}")
-        _attention_workspaces[key] = ws
+        if _capturing(index, stream):
+            raise RuntimeError("attention_workspace: this stream has none yet and is being captured; make it before the capture")
+        ws = _attention_workspaces[key] = _new_attention_workspace(index, head_dim, dtype, stream)
     return ws
 
 
@@ -582,13 +606,23 @@ def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tens
     q_start[b] .. of q) over its cached ones, themselves included: causal, with
     window > 0 only the last `window` keys and the first `sinks`. lse
     (optional, fp32 [T, q_heads]): log of the weights' sum. max_q_len: the
-    largest number of new tokens of a request."""
+    largest number of new tokens of a request.
+
+    Without workspace_buf a call uses its stream's cached workspace. One that
+    is being captured into a graph uses memory of the graph instead, and clears
+    the counters there (8 KB; a node of about 2 us), so that graphs may be
+    replayed in any order, on any stream and beside other calls; with a
+    workspace_buf of the caller's there is no such node, and what uses that
+    buffer must not overlap in time."""
     handle = _stream(q, stream)
     ws = workspace_buf
     if ws is None:
-        ws = _attention_workspaces.get((q.get_device(), handle, q.dtype, q.shape[-1]))
-        if ws is None:
-            ws = attention_workspace(q.device, q.shape[-1], q.dtype, stream)
+        if _capturing(q.get_device(), stream):
+            ws = _new_attention_workspace(q.get_device(), q.shape[-1], q.dtype, stream)
+        else:
+            ws = _attention_workspaces.get((q.get_device(), handle, q.dtype, q.shape[-1]))
+            if ws is None:
+                ws = attention_workspace(q.device, q.shape[-1], q.dtype, stream)
     st = _kv_binding.paged_attention(out, q, K_cache, V_cache, block_table, q_start, kv_len, scale, max_q_len, window,
                                      sinks, lse, ws, handle)
     if st:
@@ -663,10 +697,11 @@ class PagedKVCache:
                          stream)
 
     def attend(self, out: torch.Tensor, q: torch.Tensor, scale: float, max_q_len: int, window: int = 0,
-               sinks: int = 0, lse: Optional[torch.Tensor] = None, layer: int = 0, stream=None) -> torch.Tensor:
+               sinks: int = 0, lse: Optional[torch.Tensor] = None, layer: int = 0, stream=None,
+               workspace_buf: Optional[torch.Tensor] = None) -> torch.Tensor:
         """out = attention of the step's tokens over what their requests have cached."""
         return sgmv_paged_attention(out, q, self.K[layer], self.V[layer], self.block_table, self.q_start, self.kv_len,
-                                    scale, max_q_len, window, sinks, lse, stream=stream)
+                                    scale, max_q_len, window, sinks, lse, workspace_buf, stream)
 
 
 def sgmv_version() -> int:
@@ -680,5 +715,5 @@ __all__ = ["sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_shrink_gather", "sg
            "sgmv_pool_pointers", "sgmv_version", "workspace", "SGMVError", "lib", "EXPORTS",
            "LIBRARY", "SGMV_F32", "SGMV_BF16", "sgmv_workspace_status", "sgmv_set_wait_limit",
            "sgmv_kv_tables", "sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "attention_workspace", "PagedKVCache",
-           "SGMV_MAX_REQUESTS", "SGMV_ROPE_PLAIN", "SGMV_ROPE_LINEAR", "SGMV_ROPE_BY_PARTS",
+           "SGMV_MAX_REQUESTS", "SGMV_ATTENTION_COUNTER_BYTES", "SGMV_ROPE_PLAIN", "SGMV_ROPE_LINEAR", "SGMV_ROPE_BY_PARTS",
            "SGMV_WS_WAIT_TIMEOUT", "SGMV_WS_BAD_OFFSETS", "sgmv_fused_noalloc", "SGMV_NOALLOC_SCRATCH_BYTES"]

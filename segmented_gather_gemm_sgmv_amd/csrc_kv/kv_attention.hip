@@ -975,6 +975,7 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles
 // ----------------------------------------------------------------------------
 // The groups that a launch splits have at most 4/3 * its target parts.
 constexpr size_t kCounterBytes = (size_t)2 * kMostSplits * sizeof(uint32_t);
+static_assert(kCounterBytes == SGMV_ATTENTION_COUNTER_BYTES, "what callers clear");
 static_assert(4 * kStreamTarget <= 3 * kMostSplits && 4 * kTileTarget <= 3 * kMostSplits, "slots for every split");
 
 // The most groups of `rows` packed rows that requests of up to max_q_len
