@@ -638,8 +638,13 @@ class PagedKVCache:
     A step: ``step`` (slots for the step's new tokens, ended requests' pages
     back), then per layer ``append`` and ``attend``. Requests are the rows
     0 .. max_requests - 1; one that ended is free for another at once, its
-    pages from the next step on. Lengths and pool are kept twice and change
-    places at every step, so a step is captured in a graph two at a time."""
+    pages from the next step on.
+
+    Graphs: lengths and pool are kept twice and change places at every step,
+    so steps are captured two at a time (or another even number), and an even
+    number of other steps lies between replays. The position and slot that a
+    captured call uses stay where they are for as long as the cache lives, and
+    serve the other steps of that many tokens too."""
 
     def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_requests: int,
                  max_blocks: int, num_layers: int = 1, dtype=torch.bfloat16, device="cuda"):
@@ -657,9 +662,13 @@ class PagedKVCache:
         self.q_start = ints(max_requests + 1)
         self.position = self.slot = ints(0)
         self._slot_stream = _stream(self.slot, None)
+        self._held = {}  # by number of tokens: (position, slot, their stream) that graphs refer to
 
     def _use_slots(self, stream) -> None:
-        """Keeps position and slot, which a later step may replace, until `stream`'s work on them is done."""
+        """Keeps position and slot, which a later step may replace, until `stream`'s work on them is done; for good
+        if that work is being captured."""
+        if _capturing(self.slot.get_device(), stream):
+            self._held[self.slot.numel()] = (self.position, self.slot, self._slot_stream)
         if _stream(self.slot, stream) != self._slot_stream:
             s = _torch_stream(self.slot.device, stream)
             self.position.record_stream(s)
@@ -678,7 +687,9 @@ class PagedKVCache:
     def step(self, new_len: torch.Tensor, num_tokens: int, stream=None) -> None:
         """The next step: request b adds new_len[b] tokens (num_tokens in all),
         or has ended (new_len[b] < 0). Sets q_start, kv_len, position, slot."""
-        if self.slot.numel() != num_tokens:
+        if num_tokens in self._held:
+            self.position, self.slot, self._slot_stream = self._held[num_tokens]
+        elif self.slot.numel() != num_tokens:
             with torch.cuda.stream(_torch_stream(self.slot.device, stream)):
                 self.position = torch.empty(num_tokens, dtype=torch.int32, device=self.slot.device)
                 self.slot = torch.empty_like(self.position)

@@ -1,6 +1,7 @@
 """The paged-cache calls captured into graphs: what a graph holds is its own, in
 whatever order and beside whatever it is replayed."""
 import gc
+import weakref
 
 import numpy as np
 import pytest
@@ -97,3 +98,119 @@ def test_captured_call_with_a_workspace_of_the_callers(dev):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert int(ws[:sg.SGMV_ATTENTION_COUNTER_BYTES].sum()) == 0 and int(ws.count_nonzero()) > 0
+
+
+class Layer:
+    """One cache and what a step of it reads and writes, at fixed places per number of tokens."""
+
+    def __init__(self, dev):  # noqa: F811
+        self.dev, self.B = dev, 3
+        self.cache = sg.PagedKVCache(64, 16, 2, 64, self.B, 16, dtype=F32, device=dev)
+        self.table = sg.sgmv_rope_table(256, 64, device=dev)
+        self.io = {}
+
+    def buffers(self, T):
+        if T not in self.io:
+            self.io[T] = [torch.zeros(T, h, 64, device=self.dev) for h in (8, 2, 2, 8, 8)]
+        return self.io[T]
+
+    def fill(self, T, seed):
+        gen = torch.Generator(self.dev).manual_seed(seed)
+        for x in self.buffers(T)[:3]:
+            x.copy_(torch.randn(x.shape, generator=gen, device=self.dev))
+
+    def step(self, new, T, most):
+        q, k, v, turned, out = self.buffers(T)
+        self.cache.step(new, T)
+        self.cache.append(turned, q, k, v, self.table)
+        self.cache.attend(out, turned, 0.125, most)
+
+
+@pytest.mark.parametrize("warm", [True, False], ids=["warm", "cold"])
+def test_captured_steps_between_steps_of_other_sizes(dev, warm):  # noqa: F811
+    """Two decode steps in a graph, replayed between eager steps of another
+    number of tokens and of the same, against a second cache that takes every
+    step eagerly. What the allocator gave out in the meantime is not written."""
+    stream = torch.cuda.Stream(dev)
+    graphed, eager = Layer(dev), Layer(dev)
+    one, chunk = ints([1, 1, 1], dev), ints([9, 0, 4], dev)
+    seed = [0]
+
+    def same(T):
+        assert torch.equal(graphed.cache.kv_len, eager.cache.kv_len) and torch.equal(graphed.cache.pool, eager.cache.pool)
+        assert torch.equal(graphed.cache.block_table, eager.cache.block_table)
+        assert torch.equal(graphed.cache.K, eager.cache.K) and torch.equal(graphed.cache.V, eager.cache.V)
+        assert torch.equal(graphed.buffers(T)[4], eager.buffers(T)[4])
+
+    def both(T, f):
+        seed[0] += 1
+        for layer in (graphed, eager):
+            layer.fill(T, seed[0])
+            f(layer)
+        torch.cuda.synchronize()
+        same(T)
+
+    both(58, lambda x: x.step(ints([30, 11, 17], dev), 58, 30))
+    both(13, lambda x: x.step(chunk, 13, 9))
+    if warm:
+        stream.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(stream):
+            both(3, lambda x: x.step(one, 3, 1))
+            both(3, lambda x: x.step(one, 3, 1))
+    else:
+        graphed.buffers(3)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with capture(graph, stream):
+        for _ in range(2):
+            graphed.step(one, 3, 1)
+    slots = [weakref.ref(graphed.cache.position), weakref.ref(graphed.cache.slot)]
+    both(13, lambda x: x.step(chunk, 13, 9))
+    both(13, lambda x: x.step(chunk, 13, 9))
+    assert all(s() is not None for s in slots), "the graph's position and slot are no longer the cache's"
+    others = [torch.full((3,), 77, dtype=torch.int32, device=dev) for _ in range(2000)]
+
+    def two(layer):
+        if layer is graphed:
+            graph.replay()
+        else:
+            for _ in range(2):
+                layer.step(one, 3, 1)
+
+    for _ in range(3):
+        both(3, two)
+        both(13, lambda x: x.step(chunk, 13, 9))
+        both(13, lambda x: x.step(chunk, 13, 9))
+        both(3, lambda x: x.step(one, 3, 1))   # where the graph's slots are
+        assert graphed.cache.slot is slots[1]()
+        both(3, lambda x: x.step(one, 3, 1))
+    assert bool((torch.stack(others) == 77).all())
+    assert int(eager.cache.pool[2]) == 0
+
+
+def test_captured_layer_calls_read_the_next_steps_slots(dev):  # noqa: F811
+    """Only the layer's calls are captured: every eager step of that many
+    tokens, whatever came between, gives its slots to the graph."""
+    graphed, eager = Layer(dev), Layer(dev)
+    for x in (graphed, eager):
+        x.fill(4, 1)
+        x.step(ints([2, 2, 0], dev), 4, 2)
+    graph = torch.cuda.CUDAGraph()
+    q, k, v, turned, _ = graphed.buffers(4)
+    torch.cuda.synchronize()
+    with capture(graph):
+        graphed.cache.append(turned, q, k, v, graphed.table)
+    held = weakref.ref(graphed.cache.slot)
+    for x in (graphed, eager):
+        x.fill(1, 2)
+        x.step(ints([0, 0, 1], dev), 1, 1)
+    assert held() is not None
+    for x in (graphed, eager):
+        x.fill(4, 3)
+    graphed.cache.step(ints([1, 1, 2], dev), 4)
+    assert graphed.cache.slot is held()
+    graph.replay()
+    eager.step(ints([1, 1, 2], dev), 4, 2)
+    torch.cuda.synchronize()
+    assert torch.equal(graphed.cache.K, eager.cache.K) and torch.equal(graphed.cache.V, eager.cache.V)
+    assert torch.equal(turned, eager.buffers(4)[3])
