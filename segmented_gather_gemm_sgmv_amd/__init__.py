@@ -535,8 +535,11 @@ def sgmv_rope_table(max_position: int, rot_dim: int, base: float = 10000.0, kind
                     device="cuda", stream=None) -> torch.Tensor:
     """The rotary table [max_position, rot_dim / 2, 2] (cos, sin) that
     sgmv_rope_append takes; see include/sgmv.h for the scalings. Kept for as
-    long as the model is served."""
-    table = torch.empty((max_position, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    long as the model is served. Allocated and written on `stream` (the current
+    one, if None): work on other streams waits for that before it reads it."""
+    device = torch.device(device)
+    with torch.cuda.device(device), torch.cuda.stream(_torch_stream(device, stream)):
+        table = torch.empty((max_position, rot_dim // 2, 2), dtype=torch.float32, device=device)
     st = lib.sgmv_rope_table(_dev(table, "table"), max_position, rot_dim, base, kind, factor, beta_fast, beta_slow,
                              original_max, _stream(table, stream))
     _check("sgmv_rope_table", st)

@@ -1,0 +1,27 @@
+"""What the paged-cache calls do with memory, streams, devices, threads and
+arguments, apart from their results."""
+import pytest
+import torch
+
+import segmented_gather_gemm_sgmv_amd as sg
+
+from .test_kv_gpu import dev  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_rope_table_is_allocated_on_its_stream(dev, raw):  # noqa: F811
+    """Memory freed on the current stream, whose work there may still be
+    pending, is not what another stream writes the table to."""
+    side = torch.cuda.Stream(dev)
+    want = sg.sgmv_rope_table(30011, 128, device=dev)
+    ahead = [torch.empty_like(want) for _ in range(3)]
+    freed = {x.data_ptr() for x in ahead}
+    del ahead
+    table = sg.sgmv_rope_table(30011, 128, device=dev, stream=side.cuda_stream if raw else side)
+    assert table.data_ptr() not in freed
+    torch.cuda.synchronize()
+    assert torch.equal(table, want)
+    again = torch.empty_like(want)   # those blocks are the current stream's still
+    assert again.data_ptr() in freed
