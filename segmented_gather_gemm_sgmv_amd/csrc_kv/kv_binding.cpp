@@ -26,6 +26,12 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return t;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{};
+    return v != 0;
+}
+
 int64_t integer(PyObject *o) {
     const int64_t v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Refused{};
@@ -159,7 +165,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return sgmv_rope_append(q_out.p, q_out.stride, q.p, q.stride, size32(q_heads), k.p, k.stride, v.p, v.stride, c.K,
                                 c.V, size32(c.pages), size32(c.heads), size32(c.page), size32(D),
                                 ints(a[6], "position", T), slot, size32(T), turn, size32(max_position), size32(rot_dim),
-                                PyObject_IsTrue(a[9]) == 1, dtype_code(like), reinterpret_cast<void *>(integer(a[10])));
+                                truth(a[9]), dtype_code(like), reinterpret_cast<void *>(integer(a[10])));
     });
 }
 

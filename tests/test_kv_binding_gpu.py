@@ -25,3 +25,15 @@ def test_rope_table_is_allocated_on_its_stream(dev, raw):  # noqa: F811
     assert torch.equal(table, want)
     again = torch.empty_like(want)   # those blocks are the current stream's still
     assert again.data_ptr() in freed
+
+
+def test_a_flag_without_a_truth_value_is_refused(dev):  # noqa: F811
+    """The error is the value's own, and nothing is launched."""
+    q = torch.ones(3, 2, 64, device=dev)
+    out, pos = torch.zeros_like(q), torch.zeros(3, dtype=torch.int32, device=dev)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        sg.sgmv_rope_append(out, q, None, None, None, None, pos, None, None, torch.zeros(2))
+    torch.cuda.synchronize()
+    assert float(out.sum()) == 0
+    sg.sgmv_rope_append(out, q, None, None, None, None, pos, None, None, torch.ones(1))
+    assert torch.equal(out, q)
