@@ -540,8 +540,8 @@ def sgmv_rope_table(max_position: int, rot_dim: int, base: float = 10000.0, kind
     device = torch.device(device)
     with torch.cuda.device(device), torch.cuda.stream(_torch_stream(device, stream)):
         table = torch.empty((max_position, rot_dim // 2, 2), dtype=torch.float32, device=device)
-    st = lib.sgmv_rope_table(_dev(table, "table"), max_position, rot_dim, base, kind, factor, beta_fast, beta_slow,
-                             original_max, _stream(table, stream))
+        st = lib.sgmv_rope_table(_dev(table, "table"), max_position, rot_dim, base, kind, factor, beta_fast, beta_slow,
+                                 original_max, _stream(table, stream))
     _check("sgmv_rope_table", st)
     return table
 
@@ -635,8 +635,10 @@ def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tens
 
 class PagedKVCache:
     """Paged K and V of one or more layers, with the one block table, the ring
-    of free pages and the lengths that their requests share; all of it on the
-    device, carried from step to step without the host reading it.
+    of free pages and the lengths that their requests share; all of it on
+    `device`, which need not be the current one, carried from step to step
+    without the host reading it. Made on that device's current stream: work on
+    other streams waits for it.
 
     A step: ``step`` (slots for the step's new tokens, ended requests' pages
     back), then per layer ``append`` and ``attend``. Requests are the rows

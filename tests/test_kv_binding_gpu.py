@@ -37,3 +37,26 @@ def test_a_flag_without_a_truth_value_is_refused(dev):  # noqa: F811
     assert float(out.sum()) == 0
     sg.sgmv_rope_append(out, q, None, None, None, None, pos, None, None, torch.ones(1))
     assert torch.equal(out, q)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_a_cache_on_a_device_that_is_not_the_current_one(dev):  # noqa: F811
+    """Calls are made on their operands' device, and those of two devices are
+    refused (two ranks of one process, or a second model's cache)."""
+    here, there = [], []
+    for device, results in ((dev, here), (torch.device("cuda", 1), there)):
+        gen = torch.Generator("cpu").manual_seed(1)
+        cache = sg.PagedKVCache(64, 16, 2, 64, 2, 16, device=device)
+        table = sg.sgmv_rope_table(256, 64, device=device)
+        for new in ([40, 200], [1, 1]):
+            q, k, v = (torch.randn(sum(new), h, 64, generator=gen).bfloat16().to(device) for h in (8, 2, 2))
+            cache.step(torch.tensor(new, dtype=torch.int32, device=device), sum(new))
+            cache.append(q, q, k, v, table)
+            results.append(cache.attend(torch.empty_like(q), q, 0.125, max(new)).cpu())
+            assert torch.cuda.current_device() == 0
+    for a, b in zip(here, there):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="device"):
+        cache.step(torch.tensor([1, 1], dtype=torch.int32, device=dev), 2)
+    with pytest.raises(ValueError, match="device"):
+        cache.attend(torch.empty_like(q), q.to(dev), 0.125, 1)
