@@ -15,6 +15,14 @@ namespace {
 // An argument error: the Python exception is set.
 struct Refused {};
 
+// Python's other threads run while this lives: a launch waits where the GPU's queue is full.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 [[noreturn]] void refuse(PyObject *type, const char *name, const char *what) {
     PyErr_Format(type, "%s %s", name, what);
     throw Refused{};
@@ -130,12 +138,17 @@ PyObject *kv_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t B = x.tensor(a[0], "seq_len").numel(), T = x.tensor(a[10], "slot").numel();
         const at::Tensor &table = table2(x, a[2], B);
         const int64_t pages = x.tensor(a[4], "free_pages").numel();
+        const int32_t *seq_len = x.ints(a[0], "seq_len", B), *new_len = x.ints(a[1], "new_len", B);
+        int32_t *entries = x.ints(a[2], "block_table", -1), *ring = x.ints(a[4], "free_pages", pages);
+        const int32_t *pool_in = x.ints(a[5], "pool_in", 4);
+        int32_t *pool_out = x.ints(a[6], "pool_out", 4), *q_start = x.ints(a[7], "q_start", B + 1);
+        int32_t *kv_len = x.ints(a[8], "kv_len", B), *position = x.ints(a[9], "position", T), *slot = x.ints(a[10], "slot", T);
+        const int32_t width = size32(table.size(1)), page = size32(integer(a[3]));
+        void *stream = reinterpret_cast<void *>(integer(a[11]));
         const auto on = x.guard();
-        return sgmv_kv_tables(x.ints(a[0], "seq_len", B), x.ints(a[1], "new_len", B), size32(B), x.ints(a[2], "block_table", -1),
-                              size32(table.size(1)), size32(integer(a[3])), x.ints(a[4], "free_pages", pages), size32(pages),
-                              x.ints(a[5], "pool_in", 4), x.ints(a[6], "pool_out", 4), x.ints(a[7], "q_start", B + 1),
-                              x.ints(a[8], "kv_len", B), x.ints(a[9], "position", T), x.ints(a[10], "slot", T), size32(T),
-                              reinterpret_cast<void *>(integer(a[11])));
+        const Unlocked others;
+        return sgmv_kv_tables(seq_len, new_len, size32(B), entries, width, page, ring, size32(pages), pool_in, pool_out, q_start,
+                              kv_len, position, slot, size32(T), stream);
     });
 }
 
@@ -176,11 +189,14 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             max_position = t.size(0);
             rot_dim = 2 * t.size(1);
         }
+        const int32_t *position = x.ints(a[6], "position", T);
+        const int32_t interleaved = truth(a[9]), code = dtype_code(like);
+        void *stream = reinterpret_cast<void *>(integer(a[10]));
         const auto on = x.guard();
+        const Unlocked others;
         return sgmv_rope_append(q_out.p, q_out.stride, q.p, q.stride, size32(q_heads), k.p, k.stride, v.p, v.stride, c.K,
-                                c.V, size32(c.pages), size32(c.heads), size32(c.page), size32(D),
-                                x.ints(a[6], "position", T), slot, size32(T), turn, size32(max_position), size32(rot_dim),
-                                truth(a[9]), dtype_code(like), reinterpret_cast<void *>(integer(a[10])));
+                                c.V, size32(c.pages), size32(c.heads), size32(c.page), size32(D), position, slot, size32(T),
+                                turn, size32(max_position), size32(rot_dim), interleaved, code, stream);
     });
 }
 
@@ -208,13 +224,17 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!ws.is_contiguous()) refuse(PyExc_ValueError, "workspace", "must be contiguous");
         const double scale = PyFloat_AsDouble(a[7]);
         if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
+        const int32_t *entries = x.ints(a[4], "block_table", -1), *q_start = x.ints(a[5], "q_start", B + 1);
+        const int32_t *kv_len = x.ints(a[6], "kv_len", B);
+        const int32_t max_q_len = size32(integer(a[8])), window = size32(integer(a[9])), sinks = size32(integer(a[10]));
+        const int32_t width = size32(table.size(1)), code = dtype_code(q);
+        void *workspace = ws.data_ptr(), *stream = reinterpret_cast<void *>(integer(a[13]));
+        const size_t bytes = ws.nbytes();
         const auto on = x.guard();
+        const Unlocked others;
         return sgmv_paged_attention(outr.p, outr.stride, lse, qr.p, qr.stride, size32(heads), c.K, c.V, size32(c.pages),
-                                    size32(c.heads), size32(c.page), size32(D), x.ints(a[4], "block_table", -1),
-                                    size32(table.size(1)), x.ints(a[5], "q_start", B + 1), x.ints(a[6], "kv_len", B), size32(B),
-                                    size32(T), size32(integer(a[8])), (float)scale, size32(integer(a[9])),
-                                    size32(integer(a[10])), dtype_code(q), ws.data_ptr(), ws.nbytes(),
-                                    reinterpret_cast<void *>(integer(a[13])));
+                                    size32(c.heads), size32(c.page), size32(D), entries, width, q_start, kv_len, size32(B),
+                                    size32(T), max_q_len, (float)scale, window, sinks, code, workspace, bytes, stream);
     });
 }
 

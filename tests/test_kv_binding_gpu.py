@@ -1,5 +1,8 @@
 """What the paged-cache calls do with memory, streams, devices, threads and
 arguments, apart from their results."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -60,3 +63,36 @@ def test_a_cache_on_a_device_that_is_not_the_current_one(dev):  # noqa: F811
         cache.step(torch.tensor([1, 1], dtype=torch.int32, device=dev), 2)
     with pytest.raises(ValueError, match="device"):
         cache.attend(torch.empty_like(q), q.to(dev), 0.125, 1)
+
+
+def test_other_threads_run_while_a_launch_waits(dev):  # noqa: F811
+    """A launch waits while the GPU's queue is full (here: behind half a second
+    of other work). Python's other threads go on meanwhile."""
+    q, pos = torch.zeros(1, 1, 64, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    sg.sgmv_rope_append(q, q, None, None, None, None, pos, None, None)
+    torch.cuda.synchronize()
+    stop, gaps = threading.Event(), [0.0]
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    try:
+        torch.cuda._sleep(1_200_000_000)
+        longest = 0.0
+        for _ in range(25000):
+            began = time.perf_counter()
+            sg.sgmv_rope_append(q, q, None, None, None, None, pos, None, None)
+            longest = max(longest, time.perf_counter() - began)
+        torch.cuda.synchronize()
+    finally:
+        stop.set()
+        thread.join()
+    print(f"longest call {longest * 1e3:.0f} ms, longest gap {gaps[0] * 1e3:.0f} ms")
+    assert gaps[0] < max(0.05, longest / 3), (gaps[0], longest)
