@@ -85,10 +85,22 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
+class _NotBuilt:
+    """In the place of the paged-cache calls' binding: the package's other calls do without it."""
+
+    def __init__(self, error: ImportError):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError(f"{_HERE / '_kv_binding.so'} is not built or does not load; run "
+                          "`python -m segmented_gather_gemm_sgmv_amd.build`") from self._error
+
+
 try:
     from . import _kv_binding  # marshals the paged-cache calls; built with the library
 except ImportError as e:
-    raise ImportError(f"{_HERE / '_kv_binding.so'} is not built; run `python -m segmented_gather_gemm_sgmv_amd.build`") from e
+    _kv_binding = _NotBuilt(e)
 
 
 class SGMVError(RuntimeError):

@@ -16,6 +16,7 @@ import subprocess
 import sys
 import tempfile
 from pathlib import Path
+from typing import Optional
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -60,11 +61,19 @@ def _run(cmd, what: str, verbose: bool) -> None:
         raise RuntimeError(f"{what} failed:\n" + "\n".join(_messages(res)))
 
 
-def build_binding(library: Path = LIBRARY, verbose: bool = False) -> Path:
+def build_binding(library: Path = LIBRARY, verbose: bool = False) -> Optional[Path]:
     """Compile the Python extension that marshals the paged-cache calls (no
-    device code), linked against `library` next to it."""
+    device code), linked against `library` next to it. Without g++ or torch
+    (which the library itself does not need) it is left out: the package's
+    other calls work, those of the paged cache raise."""
+    import importlib.util
     import sysconfig
 
+    missing = [n for n, there in (("g++", shutil.which("g++")), ("torch", importlib.util.find_spec("torch"))) if not there]
+    if missing:
+        BINDING.unlink(missing_ok=True)  # one of an earlier build would not go with this library
+        print(f"{BINDING.name} is left out: no {' and no '.join(missing)}", file=sys.stderr, flush=True)
+        return None
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     inc = [f"-I{p}" for p in [INCLUDE, sysconfig.get_paths()["include"]] + list(include_paths())]
