@@ -103,9 +103,16 @@ except ImportError as e:
     _kv_binding = _NotBuilt(e)
 
 
+SGMV_ERR_ALIGN = -5
+
+
 class SGMVError(RuntimeError):
     def __init__(self, fn: str, status: int):
-        super().__init__(f"{fn}: {lib.sgmv_status_string(status).decode()} (status {status})")
+        if status == SGMV_ERR_ALIGN and fn in ("sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention"):
+            text = "an operand, or the rows of one, not 16-byte aligned"  # the library's text names the SGMV operands
+        else:
+            text = lib.sgmv_status_string(status).decode()
+        super().__init__(f"{fn}: {text} (status {status})")
         self.status = status
 
 

@@ -45,3 +45,11 @@ def test_build_without_gxx_leaves_the_module_out(tmp_path, monkeypatch, capsys):
     monkeypatch.setattr(build.shutil, "which", lambda name: None if name == "g++" else which(name))
     assert build.build_binding() is None
     assert not stale.exists() and "g++" in capsys.readouterr().err
+
+
+def test_alignment_error_names_no_operand_that_a_call_does_not_have():
+    for call in ("sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention"):
+        error = sg.SGMVError(call, -5)
+        assert error.status == -5 and "aligned" in str(error) and call in str(error)
+        assert "X, Y" not in str(error)
+    assert sg.lib.sgmv_status_string(-5).decode() in str(sg.SGMVError("sgmv_shrink", -5))
