@@ -427,6 +427,10 @@ uint32_t sgmv_set_wait_limit(uint32_t polls);
  * is refused: it gets no page and no slot and keeps its length. Requests are
  * served in order until one does not fit; after it only those that need no
  * page are. (One too long for its row of block_table takes no part in this.)
+ * The tokens of a refused request keep their rows of the step (in q_start and
+ * position) and have slot -1, the sign of it on the device. What the step's
+ * other calls write to these rows has no meaning (sgmv_paged_attention takes
+ * them to be at the end of the old length); offer them again in a later step.
  *
  * free_pages   device int32[num_pages], a ring of the free pages' ids.
  * pool_in      device int32[4]: [0] the ring's first free entry (in

@@ -710,7 +710,11 @@ class PagedKVCache:
 
     def step(self, new_len: torch.Tensor, num_tokens: int, stream=None) -> None:
         """The next step: request b adds new_len[b] tokens (num_tokens in all),
-        or has ended (new_len[b] < 0). Sets q_start, kv_len, position, slot."""
+        or has ended (new_len[b] < 0). Sets q_start, kv_len, position, slot.
+
+        A request that does not fit is refused: pool[2] counts them, its kv_len
+        stays, its tokens' slots are -1, and their rows of this step's append
+        and attend mean nothing. They are to be offered again."""
         if num_tokens in self._held:
             self.position, self.slot, self._slot_stream = self._held[num_tokens]
         elif self.slot.numel() != num_tokens:
