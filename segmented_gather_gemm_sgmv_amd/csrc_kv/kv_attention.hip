@@ -44,8 +44,10 @@ constexpr float kSlack = 8.f;
 // further tile costs 1.1 us (its loads' latency), and adding splits up 2.5:
 // kStreamMinChunk and kStreamMinTiles follow from that (one request of 2000
 // keys: 13.2 us in splits of 16 tiles, 11.0 in splits of 8).
-// fp32 chunks (16 rows at a time): 79 TFLOP/s at 4 x 256 tokens, 32 heads on
-// 8, of the 155 that a large fp32 product reaches.
+// fp32 decode, 64 requests of 2000 keys: 32 heads 648 us (6.5 TB/s), 64 heads on
+// 8 165 us (6.4). fp32 chunks: 88 to 93 TFLOP/s at 4 x 256 tokens, 32 heads on
+// 8, of the 155 that a large fp32 product reaches; each 16 rows stream the keys
+// by themselves, and a product step reads a fragment from LDS for 16 rows.
 // ----------------------------------------------------------------------------
 constexpr int kStreamRows = 16;
 constexpr int kStreamTarget = 512;   // items a launch is split into: two workgroups on each of 256 CUs
@@ -54,8 +56,10 @@ constexpr int kStreamMinTiles = 24;  // of a group that is split: fewer are done
 constexpr int kStreamMaxSplits = 256;  // of one group
 
 // bf16 requests of up to this many packed rows, two row tiles, are streamed; longer ones go to the tile kernel.
-// Measured streamed and tiled, 2000 keys, 64 heads on 8: 24 rows 15.8 and 20.9 us (4 requests), 45.9 and 50.3 (32);
-// 32 heads of their own: 32 rows 29.5 and 31.5 (4), 200 and 190 (32); 64 heads on 8: 64 rows 17.6 and 25.2, 67.8 and 61.
+// Measured streamed and tiled, 2000 keys, 4 and 32 requests, us. 64 heads on 8: 24 rows 16.7 and 23.2, 46.6 and 52.4;
+// 48 rows 18.9 and 26.3, 63.8 and 60.8; 64 rows 18.7 and 26.9, 71.9 and 64.9. 32 heads of their own: 32 rows 30.4 and
+// 32.3, 202 and 193; 48 rows 35.0 and 38.2, 269 and 205. So a few requests are better streamed up to 64 rows at least
+// (by 10 to 30%), many are not above 32 (5 to 30%); the bound is the many's, and a lone batch of few pays for it.
 constexpr int kShortRows = 32;
 
 struct StreamSmem {
@@ -127,7 +131,8 @@ __device__ __forceinline__ s16x4_t read_transposed(const void *p) {
 // Values that are not finite. In a tile that some rows see and others do not they would reach all rows, since a zero
 // weight does not take a NaN or an infinity out of a product: they enter it as 0, and are given to the rows that see
 // them afterwards (any positive weight leaves such a value what it is). Measured: the check of the tiles on the mask's
-// edge costs chunks 0 to 3%, and the test at a sum's end 0.2 us of a decode step (one request of 2000 keys: 11.3 -> 11.7 us).
+// edge costs chunks 0 to 2%, and the test at a sum's end up to 1% of them (2 x 2048 tokens, the most) and 0.2 us of a
+// decode step (one request of 2000 keys: 11.3 -> 11.7 us).
 template <typename T>
 __device__ __forceinline__ bool is_finite(T x) {
     if constexpr (sizeof(T) == 2)
@@ -595,8 +600,8 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 // ----------------------------------------------------------------------------
 // Tile kernel: bf16 groups of many rows (prompt chunks).
 //
-// What bounds it: the matrix cores, and the power they and their operands
-// take. A workgroup takes 128 packed rows, 32 per wave, against key tiles of
+// What bounds it: the matrix cores and the softmax beside them, at the clock
+// that the power limit leaves. A workgroup takes 128 packed rows, 32 per wave, against key tiles of
 // 64 that its waves share: the next tile is loaded straight to the other of
 // two LDS buffers while the present one is worked on, one barrier per tile.
 // 32 rows go through v_mfma_f32_32x32x16_bf16, whose transposed scores leave
@@ -606,17 +611,18 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 // kernel, so a request's precision does not depend on its length; the flops
 // below count the products that the operator has, not this third one.
 //
-// Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each 690
-// TFLOP/s, one prompt of 8192 tokens 740; the largest library product reaches
-// 1520. With weights of 8 bits these were 870 and 960, and the result's error
-// against 64 bits 1.4 times as large (2.3e-3 of its norm, against 1.66e-3).
-// In that form the matrix cores were busy 48% of the cycles, at 1.7 GHz with
-// random data and 2.1 with zeros, and these schedules were tried: the next
-// tile's scores formed beside this tile's softmax (886 against 867), eight
-// waves on 256 rows (+5% for long contexts, -3% for short, and 10% less at
-// heads of 64), the same with its halves taking turns (856), 64 rows per wave
-// (791; half the LDS reads, but one wave per SIMD), forced interleaving of
-// products and softmax (698).
+// Measured, heads of 128, 64 on 8: 8 x 1024 tokens behind 4096 each 1770 to
+// 1800 us, 690 to 700 TFLOP/s (1040 with the third product counted); one prompt
+// of 8192 tokens 740; the largest library product reaches 1520. The matrix cores
+// are busy 59% of the cycles. The cycles are the same with zeros for keys and
+// values, 1.47 ms at 2.1 GHz; with random data the clock is 1.64 GHz. With
+// weights of 8 bits: 870 and 960 TFLOP/s, 48% and 1.73 GHz, and the result's
+// error against 64 bits 1.4 times as large (2.3e-3 of its norm, against 1.66e-3).
+// Tried in that form, each against 867 TFLOP/s: the next tile's scores formed
+// beside this tile's softmax (886), eight waves on 256 rows (+5% for long
+// contexts, -3% for short, and 10% less at heads of 64), the same with its
+// halves taking turns (856), 64 rows per wave (791; half the LDS reads, but one
+// wave per SIMD), forced interleaving of products and softmax (698).
 // ----------------------------------------------------------------------------
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;

@@ -13,7 +13,12 @@
 // of 64 tokens already makes 256 workgroups.
 //
 // Measured: 4583 tokens of 64 + 2 x 8 heads of 128 in bf16, 190 MB, 31.4 us
-// (6.05 TB/s); 64 tokens of 32 + 2 x 32 heads 3.3 us (kernel alone).
+// (6.05 TB/s), interleaved 37.6 us (5.1), in fp32 60.1 us (6.3); 64 tokens of
+// 32 + 2 x 32 heads 3.2 us (kernel alone). A rotated part whose halves are not
+// multiples of 16 bytes moves shorter runs, v and the rest of the head with it:
+// 80 of 80 elements turned 28.1 us, 40 of 80 39.5 us; 126 of 128 107 us.
+// sgmv_rope_table: 131072 positions of 64 pairs 89 us, 94 pairs a ns, bounded by
+// pow and sincos in 64 bits; once per model.
 #include "kv_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"
