@@ -2,8 +2,8 @@
  * sgmv.h — C ABI of the MI355X (gfx950) SGMV library.
  *
  * SGMV itself comes first; the paged key/value cache that a serving layer
- * needs next to it (block tables, rotary write, attention) has its own part
- * below.
+ * needs next to it (block tables, rotary write, attention), the drafted trees
+ * over it, and tokens under several adapters each have their own parts below.
  *
  * SGMV (segmented gather matrix-vector multiplication) applies many LoRA
  * adapters to one batch in one pass. The batch's rows are grouped into
@@ -538,6 +538,199 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
 /* Workspace bytes of sgmv_paged_attention (0 on invalid arguments); the same
  * for every batch of the layout. */
 size_t sgmv_paged_attention_workspace_bytes(int32_t head_dim, int32_t dtype);
+
+/* ---------------------------------------------------------------------------
+ * Drafted trees
+ * ---------------------------------------------------------------------------
+ * A step may verify a tree of drafted tokens per request instead of adding a
+ * run of them. The step's tables are the same (sgmv_kv_tables gives every
+ * drafted token a slot, in the order of its rows); what differs is where its
+ * tokens are and what they see, and that most of them go again:
+ *   sgmv_tree_tables     once: positions (by depth) and masks, then
+ *   sgmv_rope_append     per layer, with these positions,
+ *   sgmv_tree_attention  per layer;
+ *   sgmv_tree_accept     once the model's own tokens are known: the drafted
+ *                        ones it agrees with, lengths, pages given back,
+ *   sgmv_kv_commit       the accepted tokens' keys and values to their places
+ *                        (all layers), before the next step's sgmv_kv_tables.
+ *
+ * parent        device int32[T]: for new token i of a request (row q_start[b]
+ *               + i) the index of its parent among the request's new tokens,
+ *               less than i. Any other value makes it a root: it follows the
+ *               cached tokens directly. Token 0 is the one that the model
+ *               chose last; the others are drafted.
+ * mask          device uint32[T][mask_words]: bit m % 32 of word m / 32 is the
+ *               request's new token m, set where this token sees it.
+ * mask_words    1 .. SGMV_MAX_TREE_WORDS; a tree has at most 32 * mask_words
+ *               tokens.
+ * Streams, ownership, errors and what is promised for any device-resident
+ * values are as above.
+ */
+#define SGMV_MAX_TREE_WORDS 32
+
+/*
+ * Positions and masks of one step's trees, q_start and kv_len being those of
+ * sgmv_kv_tables (kv_len with the new tokens): a token's position is
+ * kv_len[b] - n + its depth, a root's depth being 0, and its mask holds its
+ * ancestors and itself. Tokens past a request's first 32 * mask_words, and
+ * rows past the last request, have position -1 and an empty mask.
+ *
+ * position     out, int32[T]. mask: out.
+ */
+int sgmv_tree_tables(const int32_t *parent, const int32_t *q_start, const int32_t *kv_len, int32_t num_requests,
+                     int32_t *position, uint32_t *mask, int32_t mask_words, int32_t T, void *stream);
+
+/*
+ * sgmv_paged_attention with masks in the place of the causal order. With
+ * c = kv_len[b] - n cached tokens before the step, a token sees key j < c when
+ * window is 0, or j > p - window, or j < sinks, where p = c - 1 + the number
+ * of new tokens it sees (its position in a tree), and key c + m (m < n) when
+ * bit m of its mask is set. Any bits may be set, also of tokens behind it. A
+ * row that sees nothing gets out = 0 and lse = -infinity.
+ *
+ * Everything else, the workspace too, is as for sgmv_paged_attention, and:
+ * mask_words   32 * mask_words at least max_q_len.
+ * window       0, or at least max_q_len (a window then holds every drafted
+ *              token of a branch).
+ */
+int sgmv_tree_attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t q_stride,
+                        int32_t q_heads, const void *K_cache, const void *V_cache, int32_t num_pages,
+                        int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *block_table,
+                        int32_t max_blocks, const int32_t *q_start, const int32_t *kv_len, const uint32_t *mask,
+                        int32_t mask_words, int32_t num_requests, int32_t T, int32_t max_q_len, float scale,
+                        int32_t window, int32_t sinks, int32_t dtype, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/*
+ * Verification. With target[i] the model's own token after new token i (its
+ * most likely one, or one sampled from its distribution: the accepted tokens
+ * then follow that distribution), the accepted tokens of a request are token
+ * 0 and, from an accepted token i on, its first child j (parent[j] = i) with
+ * token[j] = target[i], until there is none.
+ *   path        out, int32[T]: row q_start[b] + d holds the index of request
+ *               b's accepted token d, -1 past the last one (and in rows past
+ *               the last request).
+ *   accepted    out, int32[num_requests]: how many.
+ *   next_token  out, int32[num_requests]: target of the last accepted token,
+ *               token 0 of the request's next step; -1 where there is none.
+ *   kept_len    out, int32[num_requests]: kv_len[b] - n + accepted[b].
+ * Of a request without new tokens, or that sgmv_kv_tables refused (its tokens
+ * have no slot), nothing is accepted, and its length stays. At most the first
+ * 32 * SGMV_MAX_TREE_WORDS tokens of a request are looked at.
+ *
+ * Pages that hold none of the kept_len[b] tokens go back behind the free ones
+ * of the ring, requests in order. block_table is left as it is (sgmv_kv_commit
+ * goes by slot, and entries past a request's length have no meaning to the
+ * other calls).
+ *
+ * token, target   device int32[T], any values. slot, q_start, kv_len: of the
+ *              step's sgmv_kv_tables (its outputs).
+ * free_pages, pool_in, pool_out   as for sgmv_kv_tables, pool_in being the
+ *              step's pool_out; pool_out[2] and [3] are pool_in's.
+ * The outputs must not overlap the inputs; calling twice with the same inputs
+ * gives the same result.
+ */
+int sgmv_tree_accept(const int32_t *parent, const int32_t *token, const int32_t *target, const int32_t *slot,
+                     const int32_t *q_start, const int32_t *kv_len, int32_t num_requests, int32_t page_size,
+                     const int32_t *block_table, int32_t max_blocks, int32_t *free_pages, int32_t num_pages,
+                     const int32_t *pool_in, int32_t *pool_out, int32_t *path, int32_t *accepted,
+                     int32_t *next_token, int32_t *kept_len, int32_t T, void *stream);
+
+/*
+ * Moves the accepted tokens' keys and values to where a plain step would have
+ * written them: the row at slot[q_start[b] + d] becomes what the one at
+ * slot[q_start[b] + path[q_start[b] + d]] held, in K_cache and V_cache and in
+ * every layer. path is that of sgmv_tree_accept: it grows within a request
+ * (entries that are less than their own index move nothing) and ends at its
+ * first -1; slot and q_start are the step's. Once per step: a second call
+ * would move rows again.
+ *
+ * K_cache, V_cache   num_layers caches each, layer_stride elements apart
+ *              (not read when num_layers is 1).
+ */
+int sgmv_kv_commit(void *K_cache, void *V_cache, int32_t num_layers, int64_t layer_stride, int32_t num_pages,
+                   int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *slot,
+                   const int32_t *q_start, const int32_t *path, int32_t num_requests, int32_t T, int32_t dtype,
+                   void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Several adapters per token
+ * ---------------------------------------------------------------------------
+ * The grouping that sgmv_build_segments does on the host, on the device and
+ * for a number of adapters per token, each with a weight (a mixture of
+ * adapters, whose router chose them):
+ *     Y[t] = base[t] + sum_j weight[t][j] * F_k(X[t]),  k = choice[t][j]
+ * is sgmv_sort_tokens, sgmv_spread_rows (Xs, the rows in segment order), the
+ * SGMV calls on Xs for Ys (cleared first), and sgmv_combine_rows. With one
+ * adapter per token order is the index that the gathered calls take, and no
+ * row need be moved.
+ *
+ * The gradients, given dY: of weight and of Ys, sgmv_combine_rows_grad; of Xs,
+ * the SGMV calls on dYs with A_ptrs and B_ptrs exchanged (the adapters stay as
+ * they are); of X, sgmv_combine_rows on dXs without weights, which is the
+ * gradient of sgmv_spread_rows; of base, dY.
+ *
+ * choice        device int32[T][choices]: adapters; one outside
+ *               [0, num_adapters) is no choice.
+ * place         device int32[T][choices]: the choice's row in segment order,
+ *               a negative value for none. Rows outside [0, rows) are never
+ *               followed.
+ * weight        device float[T][choices], or NULL: all 1.
+ * Xs, Ys, dYs, dXs   `rows` rows of d elements, in segment order.
+ * X, Y, base, dY, dX   T rows of d elements, in token order.
+ * Row strides are in elements; rows start 16-byte aligned. d is a positive
+ * multiple of 8, choices 1 .. SGMV_MAX_CHOICES. Sums are fp32, in the order of
+ * the choices, and rounded once. Streams, ownership, errors and what is
+ * promised for any device-resident values are as above.
+ */
+#define SGMV_MAX_CHOICES 64
+#define SGMV_MAX_SORTED_ADAPTERS 4096
+
+/*
+ * Sorts the T * choices choices by adapter, those of one adapter in their
+ * order (by token, then by choice).
+ *   order        out, int32[T * choices]: row i in segment order is choice
+ *                order[i] % choices of token order[i] / choices; -1 past the
+ *                last row.
+ *   place        out, int32[T][choices]: the inverse, -1 for no choice.
+ *   seg_start    out, int32[num_segments + 1], seg_adapter: out,
+ *                int32[num_segments]: one segment per adapter that was chosen,
+ *                adapters rising; segments past the last are empty, with
+ *                adapter 0, and seg_start's last entry is the number of rows.
+ * num_adapters  0 .. SGMV_MAX_SORTED_ADAPTERS.
+ * num_segments  at least the smaller of num_adapters and T * choices.
+ * workspace     at least sgmv_sort_tokens_workspace_bytes(...), 16-byte
+ *               aligned; what it holds before and after has no meaning. May be
+ *               NULL where that is 0. T * choices: at most 2^24.
+ */
+int sgmv_sort_tokens(const int32_t *choice, int32_t T, int32_t choices, int32_t num_adapters, int32_t *seg_start,
+                     int32_t *seg_adapter, int32_t num_segments, int32_t *order, int32_t *place, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of sgmv_sort_tokens (0 on invalid arguments, and where it
+ * needs none). */
+size_t sgmv_sort_tokens_workspace_bytes(int32_t T, int32_t choices, int32_t num_adapters);
+
+/* Xs[place[t][j]] = X[t]. Rows of Xs that no choice has are left as they were;
+ * one that two choices have holds either's. */
+int sgmv_spread_rows(void *Xs, int64_t Xs_stride, int32_t rows, const void *X, int64_t X_stride,
+                     const int32_t *place, int32_t T, int32_t choices, int32_t d, int32_t dtype, void *stream);
+
+/* Y[t] = base[t] + sum_j weight[t][j] * Ys[place[t][j]]. base: NULL (then 0),
+ * Y itself or rows of its own; Y must not overlap Ys. Choices without a row
+ * add nothing, whatever their weight. */
+int sgmv_combine_rows(void *Y, int64_t Y_stride, const void *base, int64_t base_stride, const void *Ys,
+                      int64_t Ys_stride, int32_t rows, const int32_t *place, const float *weight, int32_t T,
+                      int32_t choices, int32_t d, int32_t dtype, void *stream);
+
+/* dYs[place[t][j]] = weight[t][j] * dY[t], and dweight[t][j] = dY[t] .
+ * Ys[place[t][j]] (0 for a choice without a row). dYs or dweight may be NULL;
+ * without dweight Ys may be NULL, without dYs weight is not read. Rows of dYs
+ * that no choice has are left as they were. dYs must not overlap dY or Ys. */
+int sgmv_combine_rows_grad(void *dYs, int64_t dYs_stride, float *dweight, const void *dY, int64_t dY_stride,
+                           const void *Ys, int64_t Ys_stride, int32_t rows, const int32_t *place,
+                           const float *weight, int32_t T, int32_t choices, int32_t d, int32_t dtype,
+                           void *stream);
 
 /* A static, human-readable name for a status code. */
 const char *sgmv_status_string(int status);

@@ -4,8 +4,9 @@
 Argument marshalling only: every function below checks tensor placement,
 dtype and contiguity, passes raw device pointers, sizes and the current HIP
 stream to the C function of the same name, and raises on a non-zero status
-(the calls of the paged key/value cache through a small compiled module,
-``_kv_binding.so``, the others through ctypes).
+(the calls of the paged key/value cache, of drafted trees and of several
+adapters per token through a small compiled module, ``_kv_binding.so``, the
+others through ctypes).
 All arithmetic runs in the library's gfx950 kernels. PyTorch supplies device
 memory and streams.
 
@@ -67,6 +68,20 @@ EXPORTS = {
                                             _i32, _vp, _vp, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp, _sz,
                                             _vp]),
     "sgmv_paged_attention_workspace_bytes": (_sz, [_i32, _i32]),
+    "sgmv_tree_tables": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _vp]),
+    "sgmv_tree_attention": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                           _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _vp,
+                                           _sz, _vp]),
+    "sgmv_tree_accept": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp,
+                                        _vp, _vp, _vp, _i32, _vp]),
+    "sgmv_kv_commit": (ctypes.c_int, [_vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
+                                      _vp]),
+    "sgmv_sort_tokens": (ctypes.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "sgmv_sort_tokens_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "sgmv_spread_rows": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "sgmv_combine_rows": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "sgmv_combine_rows_grad": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32,
+                                              _i32, _vp]),
     "sgmv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sgmv_version": (ctypes.c_int, []),
 }
@@ -104,11 +119,13 @@ except ImportError as e:
 
 
 SGMV_ERR_ALIGN = -5
+_ROW_CALLS = ("sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "sgmv_tree_attention", "sgmv_kv_commit",
+              "sgmv_spread_rows", "sgmv_combine_rows", "sgmv_combine_rows_grad")  # their operands are not X, Y and V
 
 
 class SGMVError(RuntimeError):
     def __init__(self, fn: str, status: int):
-        if status == SGMV_ERR_ALIGN and fn in ("sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention"):
+        if status == SGMV_ERR_ALIGN and fn in _ROW_CALLS:
             text = "an operand, or the rows of one, not 16-byte aligned"  # the library's text names the SGMV operands
         else:
             text = lib.sgmv_status_string(status).decode()
@@ -637,19 +654,139 @@ def sgmv_paged_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tens
     and beside other calls; with a workspace_buf of the caller's there is no
     such node, and what uses that buffer must not overlap in time."""
     handle = _stream(q, stream)
-    ws = workspace_buf
-    if ws is None:
-        if _capturing(q.get_device(), stream):
-            ws = _new_attention_workspace(q.get_device(), q.shape[-1], q.dtype, stream)
-        else:
-            ws = _attention_workspaces.get((q.get_device(), handle, q.dtype, q.shape[-1]))
-            if ws is None:
-                ws = attention_workspace(q.device, q.shape[-1], q.dtype, stream)
+    ws = _attention_workspace_of(q, handle, workspace_buf, stream)
     st = _kv_binding.paged_attention(out, q, K_cache, V_cache, block_table, q_start, kv_len, scale, max_q_len, window,
                                      sinks, lse, ws, handle)
     if st:
         raise SGMVError("sgmv_paged_attention", st)
     return out
+
+
+def _attention_workspace_of(q: torch.Tensor, handle: int, workspace_buf: Optional[torch.Tensor], stream) -> torch.Tensor:
+    """The workspace of an attention call on `stream` (raw: handle)."""
+    if workspace_buf is not None:
+        return workspace_buf
+    if _capturing(q.get_device(), stream):
+        return _new_attention_workspace(q.get_device(), q.shape[-1], q.dtype, stream)
+    ws = _attention_workspaces.get((q.get_device(), handle, q.dtype, q.shape[-1]))
+    return attention_workspace(q.device, q.shape[-1], q.dtype, stream) if ws is None else ws
+
+
+# -- drafted trees -----------------------------------------------------------------
+SGMV_MAX_TREE_WORDS = 32
+
+
+def sgmv_tree_tables(parent: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, position: torch.Tensor,
+                     mask: torch.Tensor, stream=None) -> None:
+    """Positions and masks of a step that verifies a tree of drafted tokens per
+    request: parent[T] holds each new token's parent among its request's new
+    tokens (any value outside [0, its own index): none). position[T] and
+    mask[T, words] (int32; bit m % 32 of word m / 32 is new token m) are
+    written: a token is as far behind the cached ones as it is deep, and sees
+    them, its ancestors and itself."""
+    st = _kv_binding.tree_tables(parent, q_start, kv_len, position, mask, _stream(parent, stream))
+    if st:
+        raise SGMVError("sgmv_tree_tables", st)
+
+
+def sgmv_tree_attention(out: torch.Tensor, q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor,
+                        block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, mask: torch.Tensor,
+                        scale: float, max_q_len: int, window: int = 0, sinks: int = 0,
+                        lse: Optional[torch.Tensor] = None, workspace_buf: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """sgmv_paged_attention whose new tokens see, of each other, those of their
+    mask (sgmv_tree_tables, or any bits), and the tokens cached before the step
+    (with window > 0 the last `window` of what they see, and the first
+    `sinks`; a window is at least max_q_len). Workspace as there."""
+    handle = _stream(q, stream)
+    ws = _attention_workspace_of(q, handle, workspace_buf, stream)
+    st = _kv_binding.tree_attention(out, q, K_cache, V_cache, block_table, q_start, kv_len, scale, max_q_len, window,
+                                    sinks, lse, ws, handle, mask)
+    if st:
+        raise SGMVError("sgmv_tree_attention", st)
+    return out
+
+
+def sgmv_tree_accept(parent: torch.Tensor, token: torch.Tensor, target: torch.Tensor, slot: torch.Tensor,
+                     q_start: torch.Tensor, kv_len: torch.Tensor, page_size: int, block_table: torch.Tensor,
+                     free_pages: torch.Tensor, pool_in: torch.Tensor, pool_out: torch.Tensor, path: torch.Tensor,
+                     accepted: torch.Tensor, next_token: torch.Tensor, kept_len: torch.Tensor, stream=None) -> None:
+    """The drafted tokens that the model agrees with: from a request's token 0
+    on, the first child that holds target, the model's own token there. Writes
+    path (row q_start[b] + d: index of the d-th accepted token, -1 past the
+    last), accepted, next_token, kept_len and pool_out, and gives the pages past
+    kept_len back to the ring (see include/sgmv.h). Nothing is read on the host."""
+    st = _kv_binding.tree_accept(parent, token, target, slot, q_start, kv_len, page_size, block_table, free_pages, pool_in,
+                                 pool_out, path, accepted, next_token, kept_len, _stream(parent, stream))
+    if st:
+        raise SGMVError("sgmv_tree_accept", st)
+
+
+def sgmv_kv_commit(K_cache: torch.Tensor, V_cache: torch.Tensor, slot: torch.Tensor, q_start: torch.Tensor,
+                   path: torch.Tensor, stream=None) -> None:
+    """Accepted tokens' keys and values to the slots of a plain step: row
+    slot[q_start[b] + d] becomes row slot[q_start[b] + path[q_start[b] + d]].
+    One layer's caches [pages, kv_heads, page_size, head_dim], or all layers'
+    with a leading dimension. Once per sgmv_tree_accept."""
+    st = _kv_binding.kv_commit(K_cache, V_cache, slot, q_start, path, _stream(slot, stream))
+    if st:
+        raise SGMVError("sgmv_kv_commit", st)
+
+
+# -- several adapters per token ------------------------------------------------------
+SGMV_MAX_CHOICES, SGMV_MAX_SORTED_ADAPTERS = 64, 4096
+
+
+def sgmv_sort_tokens(choice: torch.Tensor, num_adapters: int, seg_start: torch.Tensor, seg_adapter: torch.Tensor,
+                     order: torch.Tensor, place: torch.Tensor, workspace_buf: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Sorts the choices [T, choices] (adapters; outside [0, num_adapters): none)
+    by adapter, on the GPU: order[i] is the choice (token * choices + which) in
+    row i, place[T, choices] each choice's row (-1: none), and seg_start,
+    seg_adapter are the segments that the SGMV calls take, the empty ones last
+    (seg_adapter holds at least min(num_adapters, T * choices) entries). With
+    one choice per token order is their `rows`."""
+    ws = workspace_buf
+    if ws is None and choice.dim() == 2:
+        need = int(lib.sgmv_sort_tokens_workspace_bytes(choice.shape[0], choice.shape[1], num_adapters))
+        if need and choice.is_cuda:  # the call's own, so that calls on other streams and replays have nothing to do with it
+            with torch.cuda.stream(None if stream is None else _torch_stream(choice.device, stream)):
+                ws = torch.empty(need, dtype=torch.uint8, device=choice.device)
+    st = _kv_binding.sort_tokens(choice, num_adapters, seg_start, seg_adapter, order, place, ws, _stream(choice, stream))
+    if st:
+        raise SGMVError("sgmv_sort_tokens", st)
+
+
+def sgmv_spread_rows(Xs: torch.Tensor, X: torch.Tensor, place: torch.Tensor, stream=None) -> torch.Tensor:
+    """Xs[place[t, j]] = X[t]: the tokens' rows in segment order. Rows that no
+    choice has are left as they were. The gradient is sgmv_combine_rows of dXs,
+    without weights."""
+    st = _kv_binding.spread_rows(Xs, X, place, _stream(X, stream))
+    if st:
+        raise SGMVError("sgmv_spread_rows", st)
+    return Xs
+
+
+def sgmv_combine_rows(Y: torch.Tensor, Ys: torch.Tensor, place: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      base: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = base[t] + sum_j weight[t, j] * Ys[place[t, j]], summed in fp32 and
+    rounded once. weight: fp32 [T, choices], None for ones; base: None for
+    zeros, Y itself, or rows of its own."""
+    st = _kv_binding.combine_rows(Y, Ys, place, weight, base, _stream(Y, stream))
+    if st:
+        raise SGMVError("sgmv_combine_rows", st)
+    return Y
+
+
+def sgmv_combine_rows_grad(dYs: Optional[torch.Tensor], dweight: Optional[torch.Tensor], dY: torch.Tensor,
+                           Ys: Optional[torch.Tensor], place: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           stream=None) -> None:
+    """Gradients of sgmv_combine_rows: dYs[place[t, j]] = weight[t, j] * dY[t] and
+    dweight[t, j] = dY[t] . Ys[place[t, j]] (fp32). Either may be None. The
+    gradient of base is dY."""
+    st = _kv_binding.combine_rows_grad(dYs, dweight, dY, Ys, place, weight, _stream(dY, stream))
+    if st:
+        raise SGMVError("sgmv_combine_rows_grad", st)
 
 
 class PagedKVCache:
@@ -664,9 +801,14 @@ class PagedKVCache:
     0 .. max_requests - 1; one that ended is free for another at once, its
     pages from the next step on.
 
-    Graphs: lengths and pool are kept twice and change places at every step,
-    so steps are captured two at a time (or another even number), and an even
-    number of other steps lies between replays. The position and slot that a
+    A step that verifies trees of drafted tokens: ``step``, then ``draft`` (positions
+    and masks), per layer ``append`` and ``attend`` with the mask, then ``accept``
+    (lengths and pages of the tokens that the model agrees with) and ``commit``.
+
+    Graphs: lengths and pool are kept twice and change places at every step and
+    every accept, so steps are captured two at a time (or another even number;
+    a drafted step with its accept is two), and an even number of other changes
+    lies between replays. The position and slot that a
     captured call uses stay where they are for as long as the cache lives, and
     serve the other steps of that many tokens too."""
 
@@ -737,10 +879,37 @@ class PagedKVCache:
 
     def attend(self, out: torch.Tensor, q: torch.Tensor, scale: float, max_q_len: int, window: int = 0,
                sinks: int = 0, lse: Optional[torch.Tensor] = None, layer: int = 0, stream=None,
-               workspace_buf: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """out = attention of the step's tokens over what their requests have cached."""
+               workspace_buf: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """out = attention of the step's tokens over what their requests have cached; with the mask of ``draft`` a
+        drafted token sees its ancestors only, of the step's tokens."""
+        if mask is not None:
+            return sgmv_tree_attention(out, q, self.K[layer], self.V[layer], self.block_table, self.q_start, self.kv_len,
+                                       mask, scale, max_q_len, window, sinks, lse, workspace_buf, stream)
         return sgmv_paged_attention(out, q, self.K[layer], self.V[layer], self.block_table, self.q_start, self.kv_len,
                                     scale, max_q_len, window, sinks, lse, workspace_buf, stream)
+
+    def draft(self, parent: torch.Tensor, mask: torch.Tensor, stream=None) -> None:
+        """The step's tokens are trees: parent[T] as for sgmv_tree_tables. Sets position (what ``append`` rotates by) and
+        writes mask [T, words]."""
+        self._use_slots(stream)
+        sgmv_tree_tables(parent, self.q_start, self.kv_len, self.position, mask, stream)
+
+    def accept(self, parent: torch.Tensor, token: torch.Tensor, target: torch.Tensor, path: torch.Tensor,
+               accepted: torch.Tensor, next_token: torch.Tensor, stream=None) -> None:
+        """Keeps, of the step's trees, what the model agrees with: target[T] is its own token after each of the step's
+        tokens. Writes path [T], accepted and next_token [max_requests] (sgmv_tree_accept); kv_len and the pool are those
+        without the other tokens from here on. Once per step, after its last ``attend``."""
+        self._use_slots(stream)
+        sgmv_tree_accept(parent, token, target, self.slot, self.q_start, self._len[0], self.page_size, self.block_table,
+                         self.free_pages, self._pool[0], self._pool[1], path, accepted, next_token, self._len[1], stream)
+        self._len.reverse()
+        self._pool.reverse()
+
+    def commit(self, path: torch.Tensor, stream=None) -> None:
+        """The accepted tokens' keys and values, of every layer, to their places. Once per ``accept``, before the next
+        ``step``."""
+        self._use_slots(stream)
+        sgmv_kv_commit(self.K, self.V, self.slot, self.q_start, path, stream)
 
 
 def sgmv_version() -> int:
@@ -755,4 +924,7 @@ __all__ = ["sgmv_shrink", "sgmv_expand", "sgmv_fused", "sgmv_shrink_gather", "sg
            "LIBRARY", "SGMV_F32", "SGMV_BF16", "sgmv_workspace_status", "sgmv_set_wait_limit",
            "sgmv_kv_tables", "sgmv_rope_table", "sgmv_rope_append", "sgmv_paged_attention", "attention_workspace", "PagedKVCache",
            "SGMV_MAX_REQUESTS", "SGMV_ATTENTION_COUNTER_BYTES", "SGMV_ROPE_PLAIN", "SGMV_ROPE_LINEAR", "SGMV_ROPE_BY_PARTS",
+           "sgmv_tree_tables", "sgmv_tree_attention", "sgmv_tree_accept", "sgmv_kv_commit", "SGMV_MAX_TREE_WORDS",
+           "sgmv_sort_tokens", "sgmv_spread_rows", "sgmv_combine_rows", "sgmv_combine_rows_grad", "SGMV_MAX_CHOICES",
+           "SGMV_MAX_SORTED_ADAPTERS",
            "SGMV_WS_WAIT_TIMEOUT", "SGMV_WS_BAD_OFFSETS", "sgmv_fused_noalloc", "SGMV_NOALLOC_SCRATCH_BYTES"]

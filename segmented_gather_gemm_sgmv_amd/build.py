@@ -3,10 +3,10 @@
 Usage: ``python segmented_gather_gemm_sgmv_amd/build.py``.
 
 The kernel file is compiled once per rank (-DSGMV_RANK=8, 16, 32, 64) and
-once more for the rank dispatch and helper kernels; these objects, the paged
-cache's and the C ABI's compile in parallel, then link into one shared library,
-against which the Python extension that marshals the paged-cache calls is
-linked.
+once more for the rank dispatch and helper kernels, the paged attention once
+for the causal call and once for drafted trees; these objects, the others' and
+the C ABI's compile in parallel, then link into one shared library, against
+which the Python extension that marshals the paged-cache calls is linked.
 """
 from __future__ import annotations
 
@@ -21,7 +21,8 @@ from typing import Optional
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"        # SGMV
-CSRC_KV = PKG / "csrc_kv"  # the paged key/value cache
+CSRC_KV = PKG / "csrc_kv"  # the paged key/value cache, and drafted trees over it
+CSRC_ROUTE = PKG / "csrc_route"  # several adapters per token
 INCLUDE = ROOT / "include"
 LIBRARY = PKG / "libsgmv.so"
 BINDING = PKG / "_kv_binding.so"  # the paged-cache calls' argument marshalling (g++, torch's headers)
@@ -29,8 +30,10 @@ BINDING = PKG / "_kv_binding.so"  # the paged-cache calls' argument marshalling 
 KERNELS = CSRC / "sgmv_kernels.hip"
 API = CSRC / "sgmv_api.cpp"
 HOST = CSRC / "sgmv_host.cpp"  # host-only entry points (no HIP): also built alone with the sanitizers
-KV = [CSRC_KV / n for n in ("kv_api.cpp", "kv_tables.hip", "kv_rope.hip", "kv_attention.hip")]
-SOURCES = [KERNELS, API, HOST, *KV]
+KV = [CSRC_KV / n for n in ("kv_api.cpp", "kv_tables.hip", "kv_rope.hip", "kv_attention.hip", "kv_tree.hip")]
+KV_ATTENTION = CSRC_KV / "kv_attention.hip"  # compiled once more for trees
+ROUTE = [CSRC_ROUTE / n for n in ("route_api.cpp", "route_sort.hip", "route_rows.hip")]
+SOURCES = [KERNELS, API, HOST, *KV, *ROUTE]
 RANKS = (8, 16, 32, 64)
 ARCH = "gfx950"
 
@@ -96,7 +99,8 @@ def build(output: Path = LIBRARY, extra_flags=(), verbose: bool = False, jobs: i
         units = [(KERNELS, [f"-DSGMV_RANK={r}"], Path(tmp) / f"kernels_r{r}.o") for r in RANKS]
         units += [(KERNELS, [], Path(tmp) / "kernels_dispatch.o"), (API, [], Path(tmp) / "api.o"),
                   (HOST, [], Path(tmp) / "host.o")]
-        units += [(src, [], Path(tmp) / f"{src.stem}.o") for src in KV]
+        units += [(src, [], Path(tmp) / f"{src.stem}.o") for src in (*KV, *ROUTE)]
+        units += [(KV_ATTENTION, ["-DSGMV_TREE"], Path(tmp) / "tree_attention.o")]
         pending = list(units)
         running = []
         failed = []

@@ -38,6 +38,54 @@ int check_rows(const void *p, int64_t stride, int32_t heads, int32_t head_dim, i
     return SGMV_OK;
 }
 
+// sgmv_paged_attention and sgmv_tree_attention.
+int attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t q_stride, int32_t q_heads,
+              const void *K_cache, const void *V_cache, int32_t num_pages, int32_t kv_heads, int32_t page_size,
+              int32_t head_dim, const int32_t *block_table, int32_t max_blocks, const int32_t *q_start,
+              const int32_t *kv_len, int32_t num_requests, int32_t T, int32_t max_q_len, float scale,
+              int32_t window, int32_t sinks, int32_t dtype, const uint32_t *mask, int32_t mask_words, bool tree,
+              void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_dtype(dtype)) return SGMV_ERR_DTYPE;
+    if (!valid_head(head_dim) || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0) return SGMV_ERR_SHAPE;
+    if (num_requests < 0 || num_requests > SGMV_MAX_REQUESTS || T < 0 || T > 1 << 24 || max_q_len < 0 ||
+        max_blocks < 0 || window < 0 || sinks < 0)
+        return SGMV_ERR_SHAPE;
+    // a tree's tokens have a bit each, and see all of their ancestors whatever the window
+    if (tree && (mask_words <= 0 || mask_words > SGMV_MAX_TREE_WORDS || max_q_len > 32 * mask_words ||
+                 (window > 0 && window < max_q_len)))
+        return SGMV_ERR_SHAPE;
+    if ((int64_t)T * q_heads > INT32_MAX || (int64_t)max_q_len * q_heads > INT32_MAX) return SGMV_ERR_SHAPE;
+    // the kernels number their items, at most these, in 31 bits
+    const int64_t rows = (int64_t)(max_q_len < T ? max_q_len : T) * (q_heads / kv_heads);
+    if (((rows / 16 + 1) * kv_heads + sgmv::kMostSplits) * num_requests > INT32_MAX) return SGMV_ERR_SHAPE;
+    int st = check_pages(num_pages, page_size);
+    if (st != SGMV_OK) return st;
+    // positions, and the ends of key tiles past them, in 31 bits; and a window past the longest context changes nothing
+    const int far = 1 << 30;
+    if ((int64_t)max_blocks * page_size > far) return SGMV_ERR_SHAPE;
+    if (!(scale > 0.f) || !isfinite(scale)) return SGMV_ERR_SHAPE;
+    if (T == 0 || num_requests == 0 || max_q_len == 0) return SGMV_OK;
+    if (!out || !q || !K_cache || !V_cache || !q_start || !kv_len || (max_blocks > 0 && !block_table) || (tree && !mask))
+        return SGMV_ERR_NULL;
+    st = check_rows(q, q_stride, q_heads, head_dim, T, dtype);
+    if (st == SGMV_OK) st = check_rows(out, out_stride, q_heads, head_dim, T, dtype);
+    if (st != SGMV_OK) return st;
+    if (!aligned16(K_cache) || !aligned16(V_cache)) return SGMV_ERR_ALIGN;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        workspace_bytes < sgmv::attention_workspace_bytes(head_dim, dtype))
+        return SGMV_ERR_WORKSPACE;
+    const sgmv::AttnArgs a{out,       out_stride,   lse,         q,        q_stride,
+                           q_heads,   q_heads / kv_heads, K_cache, V_cache, num_pages,
+                           kv_heads,  page_shift(page_size), head_dim, block_table, max_blocks,
+                           q_start,   kv_len,       num_requests, T,       max_q_len < T ? max_q_len : T,
+                           scale,     window < far ? window : far, sinks < far ? sinks : far, dtype, workspace,
+                           mask,      mask_words};
+    if ((tree ? sgmv::tree_attention_workgroups(a) : sgmv::attention_workgroups(a)) > sgmv::kMaxWorkgroups)
+        return SGMV_ERR_SHAPE;
+    const hipStream_t on = static_cast<hipStream_t>(stream);
+    return hip_status(tree ? sgmv::launch_tree_attention(a, on) : sgmv::launch_paged_attention(a, on));
+}
+
 }  // namespace
 
 extern "C" {
@@ -136,38 +184,75 @@ int sgmv_paged_attention(void *out, int64_t out_stride, float *lse, const void *
                          int32_t max_blocks, const int32_t *q_start, const int32_t *kv_len,
                          int32_t num_requests, int32_t T, int32_t max_q_len, float scale, int32_t window,
                          int32_t sinks, int32_t dtype, void *workspace, size_t workspace_bytes, void *stream) {
-    if (!valid_dtype(dtype)) return SGMV_ERR_DTYPE;
-    if (!valid_head(head_dim) || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0) return SGMV_ERR_SHAPE;
-    if (num_requests < 0 || num_requests > SGMV_MAX_REQUESTS || T < 0 || T > 1 << 24 || max_q_len < 0 ||
-        max_blocks < 0 || window < 0 || sinks < 0)
+    return attention(out, out_stride, lse, q, q_stride, q_heads, K_cache, V_cache, num_pages, kv_heads,
+                     page_size, head_dim, block_table, max_blocks, q_start, kv_len, num_requests, T, max_q_len,
+                     scale, window, sinks, dtype, nullptr, 0, false, workspace, workspace_bytes, stream);
+}
+
+int sgmv_tree_attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t q_stride,
+                        int32_t q_heads, const void *K_cache, const void *V_cache, int32_t num_pages,
+                        int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *block_table,
+                        int32_t max_blocks, const int32_t *q_start, const int32_t *kv_len, const uint32_t *mask,
+                        int32_t mask_words, int32_t num_requests, int32_t T, int32_t max_q_len, float scale,
+                        int32_t window, int32_t sinks, int32_t dtype, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    return attention(out, out_stride, lse, q, q_stride, q_heads, K_cache, V_cache, num_pages, kv_heads,
+                     page_size, head_dim, block_table, max_blocks, q_start, kv_len, num_requests, T, max_q_len,
+                     scale, window, sinks, dtype, mask, mask_words, true, workspace, workspace_bytes, stream);
+}
+
+int sgmv_tree_tables(const int32_t *parent, const int32_t *q_start, const int32_t *kv_len, int32_t num_requests,
+                     int32_t *position, uint32_t *mask, int32_t mask_words, int32_t T, void *stream) {
+    if (num_requests < 0 || num_requests > SGMV_MAX_REQUESTS || T < 0 || T > 1 << 24) return SGMV_ERR_SHAPE;
+    if (mask_words <= 0 || mask_words > SGMV_MAX_TREE_WORDS) return SGMV_ERR_SHAPE;
+    if (T == 0) return SGMV_OK;
+    if (!parent || !q_start || !position || !mask || (num_requests > 0 && !kv_len)) return SGMV_ERR_NULL;
+    const sgmv::TreeTablesArgs a{parent, q_start, kv_len, num_requests, T, position, mask, mask_words};
+    return hip_status(sgmv::launch_tree_tables(a, static_cast<hipStream_t>(stream)));
+}
+
+int sgmv_tree_accept(const int32_t *parent, const int32_t *token, const int32_t *target, const int32_t *slot,
+                     const int32_t *q_start, const int32_t *kv_len, int32_t num_requests, int32_t page_size,
+                     const int32_t *block_table, int32_t max_blocks, int32_t *free_pages, int32_t num_pages,
+                     const int32_t *pool_in, int32_t *pool_out, int32_t *path, int32_t *accepted,
+                     int32_t *next_token, int32_t *kept_len, int32_t T, void *stream) {
+    if (num_requests < 0 || num_requests > SGMV_MAX_REQUESTS || max_blocks < 0 || T < 0 || T > 1 << 24)
         return SGMV_ERR_SHAPE;
-    if ((int64_t)T * q_heads > INT32_MAX || (int64_t)max_q_len * q_heads > INT32_MAX) return SGMV_ERR_SHAPE;
-    // the kernels number their items, at most these, in 31 bits
-    const int64_t rows = (int64_t)(max_q_len < T ? max_q_len : T) * (q_heads / kv_heads);
-    if (((rows / 16 + 1) * kv_heads + sgmv::kMostSplits) * num_requests > INT32_MAX) return SGMV_ERR_SHAPE;
-    int st = check_pages(num_pages, page_size);
+    const int st = check_pages(num_pages, page_size);
     if (st != SGMV_OK) return st;
-    // positions, and the ends of key tiles past them, in 31 bits; and a window past the longest context changes nothing
-    const int far = 1 << 30;
-    if ((int64_t)max_blocks * page_size > far) return SGMV_ERR_SHAPE;
-    if (!(scale > 0.f) || !isfinite(scale)) return SGMV_ERR_SHAPE;
-    if (T == 0 || num_requests == 0 || max_q_len == 0) return SGMV_OK;
-    if (!out || !q || !K_cache || !V_cache || !q_start || !kv_len || (max_blocks > 0 && !block_table))
+    if ((int64_t)num_requests * max_blocks > INT32_MAX || (int64_t)max_blocks * page_size > INT32_MAX)
+        return SGMV_ERR_SHAPE;
+    if (!q_start || !free_pages || !pool_in || !pool_out) return SGMV_ERR_NULL;
+    if (T > 0 && (!parent || !token || !target || !slot || !path)) return SGMV_ERR_NULL;
+    if (num_requests > 0 && (!kv_len || !accepted || !next_token || !kept_len || (max_blocks > 0 && !block_table)))
         return SGMV_ERR_NULL;
-    st = check_rows(q, q_stride, q_heads, head_dim, T, dtype);
-    if (st == SGMV_OK) st = check_rows(out, out_stride, q_heads, head_dim, T, dtype);
+    const sgmv::AcceptArgs a{parent,      token,      target,     slot,      q_start, kv_len,   num_requests, T,
+                             page_shift(page_size), block_table, max_blocks, free_pages, num_pages, pool_in, pool_out, path,
+                             accepted,    next_token, kept_len};
+    return hip_status(sgmv::launch_tree_accept(a, static_cast<hipStream_t>(stream)));
+}
+
+int sgmv_kv_commit(void *K_cache, void *V_cache, int32_t num_layers, int64_t layer_stride, int32_t num_pages,
+                   int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t *slot,
+                   const int32_t *q_start, const int32_t *path, int32_t num_requests, int32_t T, int32_t dtype,
+                   void *stream) {
+    if (!valid_dtype(dtype)) return SGMV_ERR_DTYPE;
+    if (!valid_head(head_dim) || kv_heads <= 0 || kv_heads > 65536 || num_layers < 0) return SGMV_ERR_SHAPE;
+    if (num_requests < 0 || num_requests > SGMV_MAX_REQUESTS || T < 0 || T > 1 << 24) return SGMV_ERR_SHAPE;
+    const int st = check_pages(num_pages, page_size);
     if (st != SGMV_OK) return st;
-    if (!aligned16(K_cache) || !aligned16(V_cache)) return SGMV_ERR_ALIGN;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        workspace_bytes < sgmv::attention_workspace_bytes(head_dim, dtype))
-        return SGMV_ERR_WORKSPACE;
-    const sgmv::AttnArgs a{out,       out_stride,   lse,         q,        q_stride,
-                           q_heads,   q_heads / kv_heads, K_cache, V_cache, num_pages,
-                           kv_heads,  page_shift(page_size), head_dim, block_table, max_blocks,
-                           q_start,   kv_len,       num_requests, T,       max_q_len < T ? max_q_len : T,
-                           scale,     window < far ? window : far, sinks < far ? sinks : far, dtype, workspace};
-    if (sgmv::attention_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
-    return hip_status(sgmv::launch_paged_attention(a, static_cast<hipStream_t>(stream)));
+    const double layer = (double)num_pages * page_size * kv_heads * head_dim;
+    if (num_layers > 1 && ((double)layer_stride < layer || (double)layer_stride * num_layers > (double)kMaxElems))
+        return SGMV_ERR_SHAPE;
+    if (num_layers == 0 || num_requests == 0 || T == 0) return SGMV_OK;
+    if (!K_cache || !V_cache || !slot || !q_start || !path) return SGMV_ERR_NULL;
+    if (!aligned16(K_cache) || !aligned16(V_cache) || (num_layers > 1 && layer_stride * elem_size(dtype) % 16 != 0))
+        return SGMV_ERR_ALIGN;
+    const sgmv::CommitArgs a{K_cache,  V_cache, num_layers, num_layers > 1 ? layer_stride : 0, num_pages, kv_heads,
+                             page_shift(page_size), head_dim, dtype, slot, q_start, path, num_requests, T};
+    const int64_t groups = sgmv::kv_commit_workgroups(a);
+    if (groups > sgmv::kMaxWorkgroups || groups / num_requests > 65535) return SGMV_ERR_SHAPE;
+    return hip_status(sgmv::launch_kv_commit(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

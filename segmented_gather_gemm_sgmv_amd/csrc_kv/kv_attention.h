@@ -63,7 +63,7 @@ __device__ __forceinline__ TileRun tile_run(int pa, int pb, int window, int sink
     return t;
 }
 
-template <int kRows, int kKeys>
+template <bool kTree, int kRows, int kKeys>
 __device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int short_rows) {
     Share s;
     const int lo = min(max(a.q_start[b], 0), a.T), hi = min(max(a.q_start[b + 1], lo), a.T);
@@ -74,7 +74,8 @@ __device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int s
     const int64_t rows = (int64_t)s.n * a.group;
     const bool mine = rows > 0 && (take == kTakeAll || (take == kTakeShort) == (rows <= short_rows));
     s.row_tiles = mine ? (int)((rows + kRows - 1) / kRows) : 0;
-    s.tiles = mine ? tile_run<kKeys>(s.p0, s.p0 + s.n - 1, a.window, a.sinks).count : 0;
+    // A token of a tree may see any of the request's new tokens, or none: it is at p0 - 1 at least.
+    s.tiles = mine ? tile_run<kKeys>(s.p0 - kTree, s.p0 + s.n - 1, a.window, a.sinks).count : 0;
     return s;
 }
 
@@ -109,7 +110,7 @@ __device__ __forceinline__ V wave_scan(V v) {
 // metadata outside the documented ranges does that): every workgroup then
 // sees the same and none does anything. kBatch: requests per lane whose
 // lengths are read at once.
-template <int kRows, int kKeys, int kBatch>
+template <bool kTree, int kRows, int kKeys, int kBatch>
 __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                              int min_tiles, int max_splits, int index, int grid, Item &it) {
     const int lane = threadIdx.x & 63, B = a.num_requests;
@@ -119,7 +120,7 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int b = first + j0 + j;
-            s[j] = j0 + j < per && b < B ? share<kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
+            s[j] = j0 + j < per && b < B ? share<kTree, kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
         }
     };
     // The batch's work in key tiles; its rounding is the same for every wave.
@@ -157,7 +158,7 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     int b = first;
     if (kBatch > 1 && mine) {
         for (int j = 0; j < per; ++j) {
-            x = share<kRows, kKeys>(a, first + j, take, short_rows);
+            x = share<kTree, kRows, kKeys>(a, first + j, take, short_rows);
             const int splits = splits_of(x), parts = x.row_tiles * a.kv_heads * splits;
             b = first + j;
             if (at < parts) break;
@@ -182,12 +183,37 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     return true;
 }
 
-template <int kRows, int kKeys>
+template <bool kTree, int kRows, int kKeys>
 __device__ __forceinline__ bool find_item(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                           int min_tiles, int max_splits, int index, int grid, Item &it) {
     return a.num_requests <= 64
-               ? find_item_of<kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
-               : find_item_of<kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
+               ? find_item_of<kTree, kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
+               : find_item_of<kTree, kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
+}
+
+// One row's mask over its request's new tokens, which a token of a tree sees by.
+struct TreeRow {
+    const uint32_t *words;
+    int count, n;  // words, none for a row past the last; new tokens
+
+    // Bits m .. m + 31, those of tokens that there are not being 0; m is the same for every lane.
+    __device__ __forceinline__ uint32_t bits(int m) const {
+        const int left = n - m, w = m >> 5;
+        if (left <= 0 || m <= -32) return 0;
+        const uint32_t lo = (unsigned)w < (unsigned)count ? words[w] : 0, hi = (unsigned)(w + 1) < (unsigned)count ? words[w + 1] : 0;
+        const uint32_t x = __builtin_amdgcn_alignbit(hi, lo, m & 31);
+        return left < 32 ? x & ((1u << left) - 1) : x;
+    }
+    // How many it sees.
+    __device__ __forceinline__ int seen() const {
+        int sum = 0;
+        for (int m = 0; m < n; m += 32) sum += __popc(bits(m));
+        return sum;
+    }
+};
+
+__device__ __forceinline__ TreeRow tree_row(const AttnArgs &a, const Item &it, int tok, bool valid) {
+    return {a.tree + (int64_t)(it.q0 + (valid ? tok : 0)) * a.tree_words, valid ? a.tree_words : 0, it.n};
 }
 
 // Maximum and sum over the four lanes (l, l ^ 16, l ^ 32, l ^ 48) that hold

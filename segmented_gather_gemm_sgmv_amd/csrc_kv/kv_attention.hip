@@ -23,6 +23,15 @@ using namespace attn;
 
 constexpr float kSlack = 8.f;
 
+// This file is compiled twice: for the causal call, and with SGMV_TREE for sgmv_tree_attention, whose rows see the
+// keys cached before the step (their window of them) and those new tokens whose bits of their mask are set. Only key
+// tiles that reach past the cached ones look at masks.
+#ifdef SGMV_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 // ----------------------------------------------------------------------------
 // Streaming kernel: groups of few rows (decode, and every fp32 batch).
 //
@@ -330,12 +339,13 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     using S = Stream<T, D, U>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     Item it;
-    if (!find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
+    if (!find_item<kTree, kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
                                               grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
     const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
-    const int pa = it.p0 + tok_a, pb = it.p0 + tok_b;
+    // First and last position that a row has; a tree's rows are bounded together.
+    const int pa = kTree ? it.p0 - 1 : it.p0 + tok_a, pb = kTree ? it.p0 + it.n - 1 : it.p0 + tok_b;
     const TileRun run = tile_run<S::kKeys>(pa, pb, a.window, a.sinks);
     const int splits = run.count > it.size ? (run.count + it.size - 1) / it.size : 1;
     if (it.split >= splits) return;
@@ -345,9 +355,11 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     const int my = row0 + r, tok = my / a.group;
     const bool valid = my < rows;
     const int q_head = it.head * a.group + my % a.group;
-    const int pos = valid ? it.p0 + tok : -1;
+    const TreeRow mask = kTree ? tree_row(a, it, tok, valid) : TreeRow{nullptr, 0, 0};
+    const int pos = !valid ? -1 : !kTree ? it.p0 + tok : it.p0 - 1 + (a.window > 0 ? mask.seen() : 0);
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
+    const int last = kTree ? (valid ? it.p0 - 1 : -1) : pos;  // key that is seen for its position
     const int nch = a.head_dim / Elem<T>::kPerVec;
     uint4 qf[S::kUsed / 4];
     {
@@ -426,7 +438,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
                 if (!whole) {
                     if (key > pb || (key < pa_lo && key >= a.sinks))
                         vv = make_uint4(0, 0, 0, 0);  // no row sees it
-                    else if (pa != pb)  // rows of one token see the same keys
+                    else if (kTree || pa != pb)  // rows of one token see the same keys, up to its own
                         odd |= clear_nonfinite<T>(vv);
                 }
                 if (c < nch) {
@@ -458,12 +470,13 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
             }
         }
         if (!whole) {
+            const uint32_t bits = kTree && key0 + S::kKeys > it.p0 ? mask.bits(key0 - it.p0) >> (4 * g) : 0;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = key0 + 16 * nb + 4 * g + e;
-                    const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+                    const bool seen = (key <= last && (key >= w_lo || key < a.sinks)) || (bits >> (16 * nb + e) & 1);
                     s[nb][e] = seen ? s[nb][e] : kNone;
                 }
         }
@@ -533,7 +546,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
 #pragma unroll
         for (int d = 0; d < S::kOut; ++d) x[d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         each_nonfinite<T, S::kKeys>(a, it, run, first, t1, kWaves, [&](int key, const T *value) {
-            const bool seen = key <= pos && (key >= w_lo || key < a.sinks);
+            const bool seen = (key <= last && (key >= w_lo || key < a.sinks)) || (kTree && mask.bits(key - it.p0) & 1);
             if (!__any(seen)) return;
 #pragma unroll
             for (int d = 0; d < S::kOut; ++d) {
@@ -684,10 +697,11 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
-    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
+    if (!find_item<kTree, kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
-    const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
+    const int pa = kTree ? it.p0 - 1 : it.p0 + row0 / a.group;
+    const int pb = kTree ? it.p0 + it.n - 1 : it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
     const TileRun run = tile_run<kTileKeys>(pa, pb, a.window, a.sinks);
     const int splits = run.count > it.size ? (run.count + it.size - 1) / it.size : 1;
     if (it.split >= splits) return;
@@ -695,12 +709,14 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 
     const int wrow = row0 + 32 * wave;  // this wave's rows; past the last row it only helps loading
     const bool live_wave = wrow < rows;
-    const int wa = it.p0 + wrow / a.group, wb = it.p0 + (min(wrow + 32, rows) - 1) / a.group;
+    const int wa = kTree ? pa : it.p0 + wrow / a.group, wb = kTree ? pb : it.p0 + (min(wrow + 32, rows) - 1) / a.group;
     const int my = wrow + r, tok = my / a.group;
     const bool valid = my < rows;
     const int q_head = it.head * a.group + my % a.group;
-    const int pos = valid ? it.p0 + tok : -1;
+    const TreeRow mask = kTree ? tree_row(a, it, tok, valid) : TreeRow{nullptr, 0, 0};
+    const int pos = !valid ? -1 : !kTree ? it.p0 + tok : it.p0 - 1 + (a.window > 0 ? mask.seen() : 0);
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
+    const int last = kTree ? (valid ? it.p0 - 1 : -1) : pos;  // key that is seen for its position
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
     const int head_dim = kFull ? D : a.head_dim, nch = head_dim / 8;
@@ -819,13 +835,16 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(vb + v_at[d], 8 * CH * 16);
             if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t bits = kTree ? mask.bits(key0 + 32 * b - it.p0) >> (4 * h) : 0;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int key = key0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
-                        const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
+                        bool seen = (key <= last) & ((key >= w_lo) | (key < a.sinks));
+                        if (kTree) seen |= (bits >> (8 * (e / 4) + e % 4) & 1) != 0;
                         s[b][e] = seen ? s[b][e] : kNone;
                     }
+                }
             }
             float top = kNone;
 #pragma unroll
@@ -893,7 +912,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[d][e] = 0.f;
         each_nonfinite<bf16_t, kTileKeys>(a, it, run, t0, t1, 1, [&](int key, const bf16_t *value) {
-            const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
+            const bool seen = ((key <= last) & ((key >= w_lo) | (key < a.sinks))) || (kTree && mask.bits(key - it.p0) & 1);
             if (!__any(seen)) return;
 #pragma unroll
             for (int d = 0; d < L::kOut; ++d)
@@ -1022,6 +1041,7 @@ auto stream_kernel_of(const AttnArgs &a) {
 
 }  // namespace
 
+#ifndef SGMV_TREE
 size_t attention_workspace_bytes(int head_dim, int dtype) {
     const size_t d = head_dim <= 64 ? 64 : 128;
     const size_t stream = kStreamRows * d + 2 * kStreamRows;
@@ -1029,12 +1049,22 @@ size_t attention_workspace_bytes(int head_dim, int dtype) {
     return kCounterBytes + (size_t)kMostSplits * (stream + tile) * sizeof(float);
 }
 
+#endif
+
+#ifdef SGMV_TREE
+int64_t tree_attention_workgroups(const AttnArgs &a) {
+#else
 int64_t attention_workgroups(const AttnArgs &a) {
+#endif
     const Grid g = grid_of(a);
     return g.tiles + g.streams;
 }
 
+#ifdef SGMV_TREE
+hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t st) {
+#else
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
+#endif
     uint32_t *counters = static_cast<uint32_t *>(a.workspace);
     float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
     const Grid g = grid_of(a);

@@ -1,0 +1,199 @@
+// Rows to segment order and back, with weights, and the gradients
+// (sgmv_spread_rows, sgmv_combine_rows, sgmv_combine_rows_grad).
+//
+// What bounds them: HBM. A lane takes 16 bytes of a token's row: spread reads
+// them once and writes them to each of the token's rows in segment order;
+// combine reads them from each of these and writes their sum once; grad reads
+// dY's and Ys's once and keeps the products' sums. Going by tokens rather than
+// by rows in segment order, every element is read once and written once, and
+// a sum has one lane and one order.
+#include "route_launch.h"
+#include "sgmv.h"
+#include "sgmv_common.h"
+
+namespace sgmv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAtOnce = 4;  // a token's choices whose rows are read together
+
+template <typename T>
+__device__ __forceinline__ const T *row_at(const void *base, int64_t stride, int row, int vec) {
+    return static_cast<const T *>(base) + (int64_t)row * stride + vec * Elem<T>::kPerVec;
+}
+
+// Unit u of the launch: 16 bytes `vec` of token t's row. A row's units are a multiple of 64 lanes apart, or rows of few
+// units share a wave.
+struct Unit {
+    int t, vec;
+    bool on;
+};
+__device__ __forceinline__ Unit unit_of(const RowsArgs &a, int vecs, int shift, int per_row) {
+    const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    Unit x;
+    if (shift < 6) {  // 1 << shift lanes a row
+        x.t = (int)min(u >> shift, (int64_t)INT32_MAX);
+        x.vec = (int)(u & ((1 << shift) - 1));
+    } else {
+        x.t = (int)(blockIdx.x / per_row);
+        x.vec = (int)(blockIdx.x % per_row) * kThreads + threadIdx.x;
+    }
+    x.on = x.t < a.T && x.vec < vecs;
+    return x;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void spread_kernel(RowsArgs a, int vecs, int shift, int per_row) {
+    const Unit u = unit_of(a, vecs, shift, per_row);
+    if (!u.on) return;
+    const uint4 x = ld16_stream(row_at<T>(a.tokens, a.tokens_stride, u.t, u.vec));
+    const int32_t *place = a.place + (int64_t)u.t * a.choices;
+    for (int j = 0; j < a.choices; ++j) {
+        const int p = place[j];
+        if ((unsigned)p < (unsigned)a.rows) st16(const_cast<T *>(row_at<T>(a.out, a.out_stride, p, u.vec)), x);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void combine_kernel(RowsArgs a, int vecs, int shift, int per_row) {
+    constexpr int N = Elem<T>::kPerVec;
+    const Unit u = unit_of(a, vecs, shift, per_row);
+    if (!u.on) return;
+    float sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.f;
+    if (a.tokens) widen<T>(ld16(row_at<T>(a.tokens, a.tokens_stride, u.t, u.vec)), sum);
+    const int64_t at = (int64_t)u.t * a.choices;
+    for (int j0 = 0; j0 < a.choices; j0 += kAtOnce) {
+        uint4 x[kAtOnce];
+        float w[kAtOnce];
+        bool has[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int j = j0 + i;
+            const int p = j < a.choices ? a.place[at + j] : -1;
+            has[i] = (unsigned)p < (unsigned)a.rows;
+            if (has[i]) {
+                w[i] = a.weight ? a.weight[at + j] : 1.f;
+                x[i] = ld16_stream(row_at<T>(a.sorted, a.sorted_stride, p, u.vec));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (!has[i]) continue;
+            float y[N];
+            widen<T>(x[i], y);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum[e] = __builtin_fmaf(w[i], y[e], sum[e]);
+        }
+    }
+    st16(const_cast<T *>(row_at<T>(a.out, a.out_stride, u.t, u.vec)), narrow<T>(sum));
+}
+
+// A workgroup takes a token, whose row its lanes share; a choice's products are summed per lane over the row, then over
+// the wave and over the waves, in that order.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void grad_kernel(RowsArgs a, int vecs) {
+    constexpr int N = Elem<T>::kPerVec, kW = kThreads / kWave;
+    __shared__ float s_sum[kAtOnce][kW];
+    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t at = (int64_t)t * a.choices;
+    for (int j0 = 0; j0 < a.choices; j0 += kAtOnce) {
+        int p[kAtOnce];
+        float w[kAtOnce], dot[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int j = j0 + i;
+            p[i] = j < a.choices ? a.place[at + j] : -1;
+            if ((unsigned)p[i] >= (unsigned)a.rows) p[i] = -1;
+            w[i] = a.out && a.weight && p[i] >= 0 ? a.weight[at + j] : 1.f;
+            dot[i] = 0.f;
+        }
+        for (int v = tid; v < vecs; v += kThreads) {
+            float g[N];
+            widen<T>(ld16(row_at<T>(a.tokens, a.tokens_stride, t, v)), g);
+            uint4 x[kAtOnce];
+            if (a.dweight) {
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+                    if (p[i] >= 0) x[i] = ld16_stream(row_at<T>(a.sorted, a.sorted_stride, p[i], v));
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (p[i] < 0) continue;
+                float y[N];
+                if (a.out) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y[e] = w[i] * g[e];
+                    st16(const_cast<T *>(row_at<T>(a.out, a.out_stride, p[i], v)), narrow<T>(y));
+                }
+                if (a.dweight) {
+                    widen<T>(x[i], y);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) dot[i] = __builtin_fmaf(g[e], y[e], dot[i]);
+                }
+            }
+        }
+        if (!a.dweight) continue;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) dot[i] += __shfl_xor(dot[i], o);
+            if (lane == 0) s_sum[i][wave] = dot[i];
+        }
+        __syncthreads();
+        if (tid < kAtOnce && j0 + tid < a.choices) {
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < kW; ++q) sum += s_sum[tid][q];
+            a.dweight[at + j0 + tid] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+int vecs_of(const RowsArgs &a) { return a.d / (a.dtype == SGMV_BF16 ? 8 : 4); }
+
+struct Shape {
+    int vecs, shift, per_row;  // as Unit
+    int64_t blocks;
+};
+Shape shape_of(const RowsArgs &a) {
+    Shape s;
+    s.vecs = vecs_of(a);
+    s.shift = 0;
+    while (s.shift < 6 && 1 << s.shift < s.vecs) ++s.shift;
+    s.per_row = (s.vecs + kThreads - 1) / kThreads;
+    s.blocks = s.shift < 6 ? (((int64_t)a.T << s.shift) + kThreads - 1) / kThreads : (int64_t)a.T * s.per_row;
+    return s;
+}
+
+}  // namespace
+
+int64_t rows_workgroups(const RowsArgs &a) {
+    const int64_t n = shape_of(a).blocks;
+    return n > a.T ? n : a.T;
+}
+
+hipError_t launch_spread_rows(const RowsArgs &a, hipStream_t st) {
+    const Shape s = shape_of(a);
+    const auto kernel = a.dtype == SGMV_BF16 ? spread_kernel<bf16_t> : spread_kernel<float>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)s.blocks), dim3(kThreads), 0, st, a, s.vecs, s.shift, s.per_row);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_rows(const RowsArgs &a, hipStream_t st) {
+    const Shape s = shape_of(a);
+    const auto kernel = a.dtype == SGMV_BF16 ? combine_kernel<bf16_t> : combine_kernel<float>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)s.blocks), dim3(kThreads), 0, st, a, s.vecs, s.shift, s.per_row);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_rows_grad(const RowsArgs &a, hipStream_t st) {
+    const auto kernel = a.dtype == SGMV_BF16 ? grad_kernel<bf16_t> : grad_kernel<float>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)a.T), dim3(kThreads), 0, st, a, vecs_of(a));
+    return hipGetLastError();
+}
+
+}  // namespace sgmv

@@ -1,0 +1,222 @@
+// Choices sorted by adapter, on the device (sgmv_sort_tokens).
+//
+// Mathematics: a stable counting sort. With c[k] choices of adapter k and
+// C[k] = c[0] + .. + c[k-1], the i-th choice of adapter k (in the choices'
+// order) goes to row C[k] + i. A wave takes 64 choices at a time: lanes with
+// the same adapter find each other by ballots over the bits of its number, so
+// a lane's rank among them is a count of bits, and their first lane alone
+// moves the adapter's running count; nothing depends on the order of atomics.
+//
+// What bounds it: latency. Up to kOneBlock choices one workgroup does it all;
+// beyond, workgroups count a run of choices each (to the workspace), and a
+// second launch, in which every workgroup adds the others' counts up for
+// itself, places them.
+#include "route_launch.h"
+#include "sgmv.h"
+#include "sgmv_common.h"
+
+namespace sgmv {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kOneBlock = 4096;   // choices that one workgroup sorts by itself
+constexpr int kMaxBlocks = 64;
+constexpr int kRun = 1024;        // choices per workgroup, at least, where there are several
+
+struct Split {
+    int blocks, run;  // run: choices per workgroup, a multiple of kThreads
+};
+Split split_of(int n) {
+    if (n <= kOneBlock) return {1, kOneBlock};
+    int run = (n + kMaxBlocks - 1) / kMaxBlocks;
+    run = (run < kRun ? kRun : run + kThreads - 1) / kThreads * kThreads;
+    return {(n + run - 1) / run, run};
+}
+
+// Lanes of the wave whose key is this lane's, of those that have one (key >= 0).
+__device__ __forceinline__ unsigned long long same_key(int key, int bits) {
+    unsigned long long m = __ballot(key >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = key >> b & 1;
+        const unsigned long long ones = __ballot(one);
+        m &= one ? ones : ~ones;
+    }
+    return m;
+}
+
+__device__ __forceinline__ int key_of(const SortArgs &a, int i, int end) {
+    if (i >= end) return -1;
+    const int k = a.choice[i];
+    return (unsigned)k < (unsigned)a.num_adapters ? k : -1;
+}
+
+__device__ __forceinline__ unsigned long long lanes_below(int lane) { return (1ull << lane) - 1; }
+
+// LDS operations of one wave complete in order; this only keeps the compiler from moving them across.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Calls f(key, index, lanes with this key) for this wave's part [lo, hi) of the run, 64 choices at a time, in order.
+template <typename F>
+__device__ __forceinline__ void each_step(const SortArgs &a, int lo, int hi, int bits, F f) {
+    const int lane = threadIdx.x & 63;
+    for (int i0 = lo; i0 < hi; i0 += 64) {
+        const int key = key_of(a, i0 + lane, hi);
+        f(key, i0 + lane, same_key(key, bits));
+    }
+}
+
+// Counts of one run, to the workspace.
+template <int kBins>
+__global__ __launch_bounds__(kThreads) void count_kernel(SortArgs a, int run, int bits) {
+    __shared__ uint32_t s_count[kBins];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int k = tid; k < a.num_adapters; k += kThreads) s_count[k] = 0;
+    __syncthreads();
+    const int part = run / kWaves, lo = min(blockIdx.x * run + wave * part, (unsigned)a.n), hi = min(lo + part, a.n);
+    each_step(a, lo, hi, bits, [&](int key, int, unsigned long long who) {
+        if (key >= 0 && (who & lanes_below(lane)) == 0) atomicAdd(&s_count[key], (uint32_t)__popcll(who));  // a sum: in any order
+    });
+    __syncthreads();
+    for (int k = tid; k < a.num_adapters; k += kThreads) a.counts[(int64_t)blockIdx.x * a.num_adapters + k] = s_count[k];
+}
+
+// Inclusive sums of x and y over the workgroup's threads; adds them up with `base` (in, out: for the next round).
+struct Pair {
+    int x, y;
+};
+__device__ __forceinline__ Pair block_scan(Pair v, Pair (*s_wave)[kWaves], int round, Pair &total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(v.x, o), y = __shfl_up(v.y, o);
+        v.x += lane >= o ? x : 0;
+        v.y += lane >= o ? y : 0;
+    }
+    Pair *mine = s_wave[round & 1];  // the round before may still be read
+    if (lane == 63) mine[wave] = v;
+    __syncthreads();
+    total = Pair{0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) {
+            v.x += total.x;
+            v.y += total.y;
+        }
+        total.x += mine[w].x;
+        total.y += mine[w].y;
+    }
+    return v;
+}
+
+// kOne: the only workgroup, which counts for itself.
+template <int kBins, bool kOne>
+__global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, int blocks, int bits) {
+    __shared__ uint32_t s_at[kWaves][kBins];  // a wave's counts, then the rows that its next choices get
+    __shared__ Pair s_wave[2][kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, P = a.num_adapters;
+    for (int k = lane; k < P; k += 64) s_at[wave][k] = 0;
+    wave_lds_order();
+    const int part = run / kWaves, lo = min(blockIdx.x * run + wave * part, (unsigned)a.n), hi = min(lo + part, a.n);
+    each_step(a, lo, hi, bits, [&](int key, int, unsigned long long who) {
+        if (key >= 0 && (who & lanes_below(lane)) == 0) s_at[wave][key] += __popcll(who);
+        wave_lds_order();
+    });
+    __syncthreads();
+
+    // Rows before each adapter, and the segments, kThreads adapters a round.
+    Pair done = {0, 0};
+    const int rounds = (P + kThreads - 1) / kThreads;
+    for (int r = 0; r < rounds; ++r) {
+        const int k = r * kThreads + tid;
+        uint32_t here[kWaves], sum = 0, before = 0, all = 0;
+        if (k < P) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                here[w] = sum;
+                sum += s_at[w][k];
+            }
+            if constexpr (kOne) {
+                all = sum;
+            } else {
+                for (int b = 0; b < blocks; ++b) {
+                    const uint32_t c = a.counts[(int64_t)b * P + k];
+                    before += b < (int)blockIdx.x ? c : 0;
+                    all += c;
+                }
+            }
+        }
+        Pair total;
+        const Pair to = block_scan(Pair{(int)all, all > 0 ? 1 : 0}, s_wave, r, total);
+        const int start = done.x + to.x - (int)all;
+        if (k < P) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) s_at[w][k] = start + before + here[w];
+            if (blockIdx.x == 0 && all > 0) {
+                const int s = done.y + to.y - 1;
+                a.seg_start[s] = start;
+                a.seg_adapter[s] = k;
+            }
+        }
+        done.x += total.x;
+        done.y += total.y;
+    }
+    if (blockIdx.x == 0) {
+        for (int s = done.y + tid; s <= a.num_segments; s += kThreads) {
+            a.seg_start[s] = done.x;
+            if (s < a.num_segments) a.seg_adapter[s] = 0;
+        }
+    }
+    __syncthreads();
+
+    each_step(a, lo, hi, bits, [&](int key, int i, unsigned long long who) {
+        if (i < hi) {
+            int row = -1;
+            if (key >= 0) {
+                row = s_at[wave][key] + __popcll(who & lanes_below(lane));
+                a.order[row] = i;
+            }
+            a.place[i] = row;
+            if (i >= done.x) a.order[i] = -1;
+        }
+        wave_lds_order();
+        if (key >= 0 && (who & lanes_below(lane)) == 0) s_at[wave][key] += __popcll(who);
+        wave_lds_order();
+    });
+}
+
+template <int kBins>
+void launch(const SortArgs &a, Split s, int bits, hipStream_t st) {
+    if (s.blocks == 1) {
+        hipLaunchKernelGGL((place_kernel<kBins, true>), dim3(1), dim3(kThreads), 0, st, a, s.run, 1, bits);
+        return;
+    }
+    hipLaunchKernelGGL((count_kernel<kBins>), dim3(s.blocks), dim3(kThreads), 0, st, a, s.run, bits);
+    hipLaunchKernelGGL((place_kernel<kBins, false>), dim3(s.blocks), dim3(kThreads), 0, st, a, s.run, s.blocks, bits);
+}
+
+}  // namespace
+
+size_t sort_workspace_bytes(int n, int num_adapters) {
+    const Split s = split_of(n);
+    return s.blocks == 1 ? 0 : (size_t)s.blocks * num_adapters * sizeof(uint32_t);
+}
+
+hipError_t launch_sort_tokens(const SortArgs &a, hipStream_t st) {
+    int bits = 0;
+    while (1 << bits < a.num_adapters) ++bits;
+    const Split s = split_of(a.n);
+    if (a.num_adapters <= 256)
+        launch<256>(a, s, bits, st);
+    else if (a.num_adapters <= 1024)
+        launch<1024>(a, s, bits, st);
+    else
+        launch<SGMV_MAX_SORTED_ADAPTERS>(a, s, bits, st);
+    return hipGetLastError();
+}
+
+}  // namespace sgmv
