@@ -109,8 +109,8 @@ __device__ __forceinline__ V wave_scan(V v) {
 // (the grid is an upper bound), or if the items do not fit the grid (only
 // metadata outside the documented ranges does that): every workgroup then
 // sees the same and none does anything. kBatch: requests per lane whose
-// lengths are read at once.
-template <bool kTree, int kRows, int kKeys, int kBatch>
+// lengths are read at once. kSplit: only the items of groups that are split.
+template <bool kTree, bool kSplit, int kRows, int kKeys, int kBatch>
 __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                              int min_tiles, int max_splits, int index, int grid, Item &it) {
     const int lane = threadIdx.x & 63, B = a.num_requests;
@@ -138,28 +138,61 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     const auto splits_of = [&](const Share &x) {
         return x.tiles < min_tiles ? 1 : min(max((x.tiles + chunk / 2) / chunk, 1), max_splits);
     };
-    int items = 0, slots = 0;
-    for (int j0 = 0; j0 < per; j0 += kBatch) {
-        if (per > kBatch) read(j0);
+    // Requests in their order, or a tree launch's in four classes by their tiles, the longest first, where its items
+    // take the GPU's workgroups more than once: a long one that starts last would leave the others idle.
+    const auto parts_of = [&](const Share &x, int splits) { return kSplit && splits == 1 ? 0 : x.row_tiles * a.kv_heads * splits; };
+    int top = 0, classes = 1;
+    if constexpr (kTree) {
+        if (per <= kBatch) {
+            int all = 0;
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int splits = splits_of(s[j]), parts = s[j].row_tiles * a.kv_heads * splits;
-            items += parts;
-            slots += splits > 1 ? parts : 0;
+            for (int j = 0; j < kBatch; ++j) {
+                top = max(top, s[j].tiles);
+                all += s[j].row_tiles * a.kv_heads * splits_of(s[j]);
+            }
+            all = __builtin_amdgcn_readlane(wave_scan(all), 63);
+            if (!kSplit && all > grid) return false;
+            if (all > target) classes = 4;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) top = max(top, __shfl_xor(top, o));
         }
     }
-    const int items_to = wave_scan(items), slots_to = wave_scan(slots);
-    if (__builtin_amdgcn_readlane(items_to, 63) > grid) return false;
-    int at = index - (items_to - items), slot = slots_to - slots;
-    bool mine = at >= 0 && at < items;
-    const unsigned long long who = __ballot(mine);
-    if (who == 0) return false;
+    const auto class_of = [&](const Share &x) {
+        return classes == 1 ? 0 : (4 * x.tiles > top) + (4 * x.tiles > 2 * top) + (4 * x.tiles > 3 * top);
+    };
+    int at = 0, slot = 0, items_before = 0, slots_before = 0, which = classes - 1;
+    bool mine = false;
+    unsigned long long who = 0;
+    for (; which >= 0; --which) {
+        int items = 0, slots = 0;
+        for (int j0 = 0; j0 < per; j0 += kBatch) {
+            if (per > kBatch) read(j0);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int splits = splits_of(s[j]), parts = class_of(s[j]) == which ? parts_of(s[j], splits) : 0;
+                items += parts;
+                slots += splits > 1 ? parts : 0;
+            }
+        }
+        const int items_to = wave_scan(items), slots_to = wave_scan(slots);
+        if (who == 0) {
+            at = index - items_before - (items_to - items);
+            slot = slots_before + slots_to - slots;
+            mine = at >= 0 && at < items;
+            who = __ballot(mine);
+        }
+        items_before += __builtin_amdgcn_readlane(items_to, 63);
+        slots_before += __builtin_amdgcn_readlane(slots_to, 63);
+        if (who != 0 && classes > 1) break;
+    }
+    if (who == 0 || items_before > grid) return false;
     Share x = s[0];
     int b = first;
     if (kBatch > 1 && mine) {
         for (int j = 0; j < per; ++j) {
-            x = share<kTree, kRows, kKeys>(a, first + j, take, short_rows);
-            const int splits = splits_of(x), parts = x.row_tiles * a.kv_heads * splits;
+            const Share y = share<kTree, kRows, kKeys>(a, first + j, take, short_rows);
+            const int splits = splits_of(y), parts = class_of(y) == which ? parts_of(y, splits) : 0;
+            x = y;
             b = first + j;
             if (at < parts) break;
             at -= parts;
@@ -183,12 +216,12 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     return true;
 }
 
-template <bool kTree, int kRows, int kKeys>
+template <bool kTree, bool kSplit, int kRows, int kKeys>
 __device__ __forceinline__ bool find_item(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                           int min_tiles, int max_splits, int index, int grid, Item &it) {
     return a.num_requests <= 64
-               ? find_item_of<kTree, kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
-               : find_item_of<kTree, kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
+               ? find_item_of<kTree, kSplit, kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
+               : find_item_of<kTree, kSplit, kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
 }
 
 // One row's mask over its request's new tokens, which a token of a tree sees by.

@@ -12,6 +12,8 @@
 // row's maximum is a maximum over a lane's registers and two or one lane
 // swaps), the scores leave the first product in the layout in which the second
 // takes its weights, and the order of keys within a product is free.
+#include <type_traits>
+
 #include "kv_attention.h"
 #include "sgmv.h"
 
@@ -339,7 +341,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     using S = Stream<T, D, U>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
     Item it;
-    if (!find_item<kTree, kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
+    if (!find_item<kTree, false, kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
                                               grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
@@ -602,7 +604,7 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
             }
         }
     }
-    if (splits == 1) return;
+    if (kTree || splits == 1) return;  // a tree's splits are added up by a launch of their own
 
     uint32_t *counter = counters + it.first_slot;
     if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
@@ -697,7 +699,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
-    if (!find_item<kTree, kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
+    if (!find_item<kTree, false, kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
     const int pa = kTree ? it.p0 - 1 : it.p0 + row0 / a.group;
@@ -707,7 +709,11 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     if (it.split >= splits) return;
     const int t0 = it.split * it.size, t1 = min(run.count, t0 + it.size);
 
-    const int wrow = row0 + 32 * wave;  // this wave's rows; past the last row it only helps loading
+    // Trees' tiles of up to 64 rows: two waves have the rows, for the first half of each key tile's keys, and two have
+    // them for the second half.
+    const bool halves = kTree && rows - row0 <= kTileRows / 2;
+    const int row_block = halves ? wave & 1 : wave, key_block = halves ? wave >> 1 : 0;
+    const int wrow = row0 + 32 * row_block;  // this wave's rows; past the last row it only helps loading
     const bool live_wave = wrow < rows;
     const int wa = kTree ? pa : it.p0 + wrow / a.group, wb = kTree ? pb : it.p0 + (min(wrow + 32, rows) - 1) / a.group;
     const int my = wrow + r, tok = my / a.group;
@@ -794,7 +800,9 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     const auto all_see = [&](int key0) {  // every row sees every key of the tile
         return key0 + kTileKeys - 1 <= pa && (pb_lo <= key0 || key0 + kTileKeys <= a.sinks);
     };
-    auto step = [&](int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
+    // kBlocks: 32-key blocks of a tile that a wave takes, from key_block on.
+    auto step = [&](auto blocks, int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
+        constexpr int kBlocks = decltype(blocks)::value;
         if (i + 1 < n) {
             if ((i + 1) % 16 == 0) load_pages(i + 1);
             load_tile(i + 1, k_next, v_next);
@@ -814,32 +822,35 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             lds_barrier();
         }
         if (live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks)) {
-            bf16x8_t kf[2][L::kSteps];
+            const int first = kBlocks == 1 ? key_block : 0;  // 32-key block
+            const unsigned char *k_from = kb + first * 32 * CH * 16, *v_from = vb + first * 32 * CH * 16;
+            bf16x8_t kf[kBlocks][L::kSteps];
 #pragma unroll
-            for (int k = 0; k < L::kSteps; ++k) kf[0][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
-            for (int k = 0; k < L::kSteps; ++k) kf[1][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k] + 32 * CH * 16);
-            __builtin_amdgcn_sched_barrier(0);
-            f32x16_t s[2];
+                for (int k = 0; k < L::kSteps; ++k) kf[b][k] = *reinterpret_cast<const bf16x8_t *>(k_from + k_at[k] + b * 32 * CH * 16);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            f32x16_t s[kBlocks];
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < L::kSteps; ++k) s[0] = mfma32(kf[0][k], qf[k], s[0]);
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-            for (int k = 0; k < L::kSteps; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
+                for (int k = 0; k < L::kSteps; ++k) s[b] = mfma32(kf[b][k], qf[k], s[b]);
             bf16x8_t vf[2][L::kOut];  // V fragments of two 16-key steps
 #pragma unroll
-            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(vb + v_at[d], 8 * CH * 16);
+            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(v_from + v_at[d], 8 * CH * 16);
             if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t bits = kTree ? mask.bits(key0 + 32 * b - it.p0) >> (4 * h) : 0;
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int key_b = key0 + 32 * (first + b);
+                    const uint32_t bits = kTree ? mask.bits(key_b - it.p0) >> (4 * h) : 0;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int key = key0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
+                        const int key = key_b + 8 * (e / 4) + 4 * h + e % 4;
                         bool seen = (key <= last) & ((key >= w_lo) | (key < a.sinks));
                         if (kTree) seen |= (bits >> (8 * (e / 4) + e % 4) & 1) != 0;
                         s[b][e] = seen ? s[b][e] : kNone;
@@ -848,7 +859,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             }
             float top = kNone;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
             top = swap32_max(top) * c2;
@@ -863,7 +874,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             }
             const float ref = ref_of(m);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
+            for (int t = 0; t < 2 * kBlocks; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
                 float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -875,10 +886,10 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
                 for (int i = 0; i < 4; ++i) split_weights(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
                 const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 const bf16x8_t p_lo = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                if (t < 3) {
+                if (t + 1 < 2 * kBlocks) {
 #pragma unroll
                     for (int d = 0; d < L::kOut; ++d)
-                        vf[(t + 1) & 1][d] = read_columns(vb + v_at[d] + 16 * (t + 1) * CH * 16, 8 * CH * 16);
+                        vf[(t + 1) & 1][d] = read_columns(v_from + v_at[d] + 16 * (t + 1) * CH * 16, 8 * CH * 16);
                 }
 #pragma unroll
                 for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p, o[d]);
@@ -894,18 +905,48 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
         load_tile(0, k_even, v_even);
     }
     loads_barrier();
-    for (int i = 0; i < n; i += 2) {
-        step(i, k_even, v_even, k_odd, v_odd);
-        if (i + 1 < n) step(i + 1, k_odd, v_odd, k_even, v_even);
-    }
+    const auto steps = [&](auto blocks) {
+        for (int i = 0; i < n; i += 2) {
+            step(blocks, i, k_even, v_even, k_odd, v_odd);
+            if (i + 1 < n) step(blocks, i + 1, k_odd, v_odd, k_even, v_even);
+        }
+    };
+    if (halves)
+        steps(std::integral_constant<int, 1>{});
+    else
+        steps(std::integral_constant<int, 2>{});
     l = swap32_sum(l);
+    if (halves) {  // the second halves' results, to the waves with the first
+        float *there = reinterpret_cast<float *>(row_block == 0 ? k_even : v_even) + lane;
+        float *more = reinterpret_cast<float *>(k_odd) + row_block * 128 + lane;
+        if (key_block == 1) {
+#pragma unroll
+            for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) there[(16 * d + e) * 64] = o[d][e];
+            more[0] = m;
+            more[64] = l;
+        }
+        lds_barrier();
+        if (key_block == 0) {
+            const float m2 = more[0], top = fmaxf(m, m2);
+            const float keep = exp2_fast(m - ref_of(top)), keep2 = exp2_fast(m2 - ref_of(top));
+            m = top;
+            l = l * keep + more[64] * keep2;
+#pragma unroll
+            for (int d = 0; d < L::kOut; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * keep + there[(16 * d + e) * 64] * keep2;
+        }
+    }
+    const bool mine = valid && key_block == 0;  // this wave has its rows' results
     // A sum over a value that is not finite is that value, which was cleared, or met a weight's zero low part.
     bool odd = sm.odd != 0;
 #pragma unroll
     for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) odd |= o[d][e] != o[d][e];
-    if (__any(odd && valid && l == l)) {
+    if (__any(odd && mine && l == l)) {
         f32x16_t x[L::kOut];
 #pragma unroll
         for (int d = 0; d < L::kOut; ++d)
@@ -934,10 +975,10 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 
     const __amdgpu_buffer_rsrc_t part =
         part_rsrc(slots + (int64_t)it.first_slot * L::kSlotFloats, (uint32_t)splits * L::kSlotFloats * 4);
-    if (valid) {
+    if (mine) {
         const int64_t q_row = it.q0 + tok;
         const uint32_t slot = (uint32_t)it.split * L::kSlotFloats * 4;
-        const int row = 32 * wave + r;
+        const int row = 32 * row_block + r;
 #pragma unroll
         for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
@@ -959,7 +1000,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             }
         }
     }
-    if (splits == 1) return;
+    if (kTree || splits == 1) return;
 
     uint32_t *counter = counters + it.first_slot;
     if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
@@ -1039,6 +1080,109 @@ auto stream_kernel_of(const AttnArgs &a) {
     return once ? stream_kernel<T, 128, 128, true> : stream_kernel<T, 128, 128, false>;
 }
 
+
+#ifdef SGMV_TREE
+// ----------------------------------------------------------------------------
+// Adding up the splits of a tree's groups, in a launch of its own: a group of
+// 128 rows in 32 splits is 2 MB, which the last of its workgroups alone would
+// read at the latency of 16 loads a lane (one request of 25 tokens behind
+// 31000, 64 heads on 8: 106 us in all). Here split k's workgroup adds the k-th
+// part of the group's rows, a wave a row; the workgroups look for their groups
+// as the attention's do.
+// ----------------------------------------------------------------------------
+template <typename T, int D, int kRows, int kKeys, int kMaxSplits>
+__device__ __forceinline__ void join_item(const AttnArgs &a, int take, int target, int min_chunk, int min_tiles, int index,
+                                          const float *slots) {
+    constexpr int kSlot = kRows * D + 2 * kRows, kPer = D / 64, kRegs = (kMaxSplits + 63) / 64, kDeep = 16;
+    Item it;
+    if (!find_item<true, true, kRows, kKeys>(a, take, kShortRows, target, min_chunk, min_tiles, kMaxSplits, index, kMostSplits, it))
+        return;
+    const TileRun run = tile_run<kKeys>(it.p0 - 1, it.p0 + it.n - 1, a.window, a.sinks);
+    const int splits = (run.count + it.size - 1) / it.size;
+    if (it.split >= splits) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row0 = it.row_tile * kRows, live = min(kRows, it.n * a.group - row0);
+    const float *part = slots + (int64_t)it.first_slot * kSlot;
+    for (int row = live * it.split / splits + wave; row < live * (it.split + 1) / splits; row += kWaves) {
+        float f[kRegs], l[kRegs], top = kNone, weight = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+            const int k = 64 * i + lane;
+            f[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + row] : kNone;
+            l[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + kRows + row] : 0.f;
+            top = fmaxf(top, f[i]);
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+            f[i] = exp2_fast(f[i] - ref_of(top));
+            weight += f[i] * l[i];
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) weight += __shfl_xor(weight, o);
+        float sum[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) sum[c] = 0.f;
+        const float *from = part + (int64_t)row * D + kPer * lane;
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+            for (int k0 = 64 * i; k0 < min(splits, 64 * i + 64); k0 += kDeep) {
+                float x[kDeep][kPer];
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j)
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) x[j][c] = from[(int64_t)min(k0 + j, splits - 1) * kSlot + c];
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j) {
+                    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[i]), (k0 + j) & 63));
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c)  // a value that is not finite is that value under any weight
+                        sum[c] += k0 + j >= splits ? 0.f : is_finite(x[j][c]) ? x[j][c] * w : x[j][c];
+                }
+            }
+        }
+        const int at = row0 + row, head = it.head * a.group + at % a.group, col = kPer * lane;
+        const int64_t q_row = it.q0 + at / a.group;
+        const float inv = weight > 0.f || weight != weight ? 1.f / weight : 0.f;
+        if (col < a.head_dim) {
+            T *dst = static_cast<T *>(a.out) + q_row * a.out_stride + (int64_t)head * a.head_dim + col;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                if constexpr (sizeof(T) == 2)
+                    dst[c].bits = __builtin_bit_cast(uint16_t, (__bf16)(sum[c] * inv));
+                else
+                    dst[c] = sum[c] * inv;
+            }
+        }
+        if (a.lse && lane == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
+    }
+}
+
+// Workgroups below `tiles` (0 or kMostSplits) join the tile kernel's groups, the others the streamed ones.
+template <typename T, int D, int U>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int tiles, int take_tiles, const float *slots) {
+    const int index = blockIdx.x;
+    if constexpr (sizeof(T) == 2) {
+        if (index < tiles) {
+            join_item<T, D, kTileRows, kTileKeys, kTileMaxSplits>(a, take_tiles, kTileTarget, kTileMinChunk, kTileMinTiles, index, slots);
+            return;
+        }
+    }
+    const float *mine = slots + (tiles > 0 ? (int64_t)kMostSplits * Tile<D>::kSlotFloats : 0);
+    join_item<T, D, kStreamRows, Stream<T, D, U>::kKeys, kStreamMaxSplits>(a, tiles > 0 ? kTakeShort : kTakeAll, kStreamTarget,
+                                                                         kStreamMinChunk, kStreamMinTiles, index - tiles, mine);
+}
+
+// The most key tiles that a group of the call can have.
+int64_t most_tiles(const AttnArgs &a, int keys) {
+    const int64_t all = (((int64_t)a.max_blocks << a.page_shift) + keys - 1) / keys;
+    if (a.window == 0) return all;
+    const int64_t seen = ((int64_t)a.window + a.max_q_len) / keys + 2 + ((int64_t)a.sinks + keys - 1) / keys;
+    return seen < all ? seen : all;
+}
+#endif
+
 }  // namespace
 
 #ifndef SGMV_TREE
@@ -1080,6 +1224,20 @@ hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
                                                 : tile_kernel<128, 128, false>;
         hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a, (int)g.tiles, counters, slots);
     }
+#ifdef SGMV_TREE
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const bool bf16 = a.dtype == SGMV_BF16;
+    const bool tiles = g.tiles > 0 && most_tiles(a, kTileKeys) >= kTileMinTiles;
+    const bool streams = (g.tiles == 0 || g.streams > 0) && most_tiles(a, bf16 ? 32 : 16) >= kStreamMinTiles;
+    if (tiles || streams) {
+        const int tile_groups = g.tiles > 0 ? kMostSplits : 0;
+        const auto join = bf16 ? (a.head_dim <= 64 ? join_kernel<bf16_t, 64, 64> : join_kernel<bf16_t, 128, 128>)
+                               : (a.head_dim <= 64 ? join_kernel<float, 64, 64> : join_kernel<float, 128, 128>);
+        hipLaunchKernelGGL(join, dim3(tile_groups + (streams ? kMostSplits : 0)), dim3(kThreads), 0, st, a, tile_groups,
+                           g.streams == 0 ? kTakeAll : kTakeLong, slots);
+    }
+#endif
     return hipGetLastError();
 }
 
