@@ -64,10 +64,10 @@ __device__ __forceinline__ TileRun tile_run(int pa, int pb, int window, int sink
 }
 
 template <bool kTree, int kRows, int kKeys>
-__device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int short_rows) {
+__device__ __forceinline__ Share share_of(const AttnArgs &a, int q_start, int q_end, int kv_len, int take, int short_rows) {
     Share s;
-    const int lo = min(max(a.q_start[b], 0), a.T), hi = min(max(a.q_start[b + 1], lo), a.T);
-    const int kv = min(max(a.kv_len[b], 0), a.max_blocks << a.page_shift);
+    const int lo = min(max(q_start, 0), a.T), hi = min(max(q_end, lo), a.T);
+    const int kv = min(max(kv_len, 0), a.max_blocks << a.page_shift);
     s.q0 = lo;
     s.n = min(hi - lo, a.max_q_len);
     s.p0 = kv - (hi - lo);  // below 0 by at most T: such a token sees nothing
@@ -77,6 +77,11 @@ __device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int s
     // A token of a tree may see any of the request's new tokens, or none: it is at p0 - 1 at least.
     s.tiles = mine ? tile_run<kKeys>(s.p0 - kTree, s.p0 + s.n - 1, a.window, a.sinks).count : 0;
     return s;
+}
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ Share share(const AttnArgs &a, int b, int take, int short_rows) {
+    return share_of<false, kRows, kKeys>(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], take, short_rows);
 }
 
 struct Item {
@@ -109,8 +114,8 @@ __device__ __forceinline__ V wave_scan(V v) {
 // (the grid is an upper bound), or if the items do not fit the grid (only
 // metadata outside the documented ranges does that): every workgroup then
 // sees the same and none does anything. kBatch: requests per lane whose
-// lengths are read at once. kSplit: only the items of groups that are split.
-template <bool kTree, bool kSplit, int kRows, int kKeys, int kBatch>
+// lengths are read at once.
+template <int kRows, int kKeys, int kBatch>
 __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                              int min_tiles, int max_splits, int index, int grid, Item &it) {
     const int lane = threadIdx.x & 63, B = a.num_requests;
@@ -120,7 +125,7 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int b = first + j0 + j;
-            s[j] = j0 + j < per && b < B ? share<kTree, kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
+            s[j] = j0 + j < per && b < B ? share<kRows, kKeys>(a, b, take, short_rows) : Share{0, 0, 0, 0, 0};
         }
     };
     // The batch's work in key tiles; its rounding is the same for every wave.
@@ -138,61 +143,28 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     const auto splits_of = [&](const Share &x) {
         return x.tiles < min_tiles ? 1 : min(max((x.tiles + chunk / 2) / chunk, 1), max_splits);
     };
-    // Requests in their order, or a tree launch's in four classes by their tiles, the longest first, where its items
-    // take the GPU's workgroups more than once: a long one that starts last would leave the others idle.
-    const auto parts_of = [&](const Share &x, int splits) { return kSplit && splits == 1 ? 0 : x.row_tiles * a.kv_heads * splits; };
-    int top = 0, classes = 1;
-    if constexpr (kTree) {
-        if (per <= kBatch) {
-            int all = 0;
+    int items = 0, slots = 0;
+    for (int j0 = 0; j0 < per; j0 += kBatch) {
+        if (per > kBatch) read(j0);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                top = max(top, s[j].tiles);
-                all += s[j].row_tiles * a.kv_heads * splits_of(s[j]);
-            }
-            all = __builtin_amdgcn_readlane(wave_scan(all), 63);
-            if (!kSplit && all > grid) return false;
-            if (all > target) classes = 4;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) top = max(top, __shfl_xor(top, o));
+        for (int j = 0; j < kBatch; ++j) {
+            const int splits = splits_of(s[j]), parts = s[j].row_tiles * a.kv_heads * splits;
+            items += parts;
+            slots += splits > 1 ? parts : 0;
         }
     }
-    const auto class_of = [&](const Share &x) {
-        return classes == 1 ? 0 : (4 * x.tiles > top) + (4 * x.tiles > 2 * top) + (4 * x.tiles > 3 * top);
-    };
-    int at = 0, slot = 0, items_before = 0, slots_before = 0, which = classes - 1;
-    bool mine = false;
-    unsigned long long who = 0;
-    for (; which >= 0; --which) {
-        int items = 0, slots = 0;
-        for (int j0 = 0; j0 < per; j0 += kBatch) {
-            if (per > kBatch) read(j0);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int splits = splits_of(s[j]), parts = class_of(s[j]) == which ? parts_of(s[j], splits) : 0;
-                items += parts;
-                slots += splits > 1 ? parts : 0;
-            }
-        }
-        const int items_to = wave_scan(items), slots_to = wave_scan(slots);
-        if (who == 0) {
-            at = index - items_before - (items_to - items);
-            slot = slots_before + slots_to - slots;
-            mine = at >= 0 && at < items;
-            who = __ballot(mine);
-        }
-        items_before += __builtin_amdgcn_readlane(items_to, 63);
-        slots_before += __builtin_amdgcn_readlane(slots_to, 63);
-        if (who != 0 && classes > 1) break;
-    }
-    if (who == 0 || items_before > grid) return false;
+    const int items_to = wave_scan(items), slots_to = wave_scan(slots);
+    if (__builtin_amdgcn_readlane(items_to, 63) > grid) return false;
+    int at = index - (items_to - items), slot = slots_to - slots;
+    bool mine = at >= 0 && at < items;
+    const unsigned long long who = __ballot(mine);
+    if (who == 0) return false;
     Share x = s[0];
     int b = first;
     if (kBatch > 1 && mine) {
         for (int j = 0; j < per; ++j) {
-            const Share y = share<kTree, kRows, kKeys>(a, first + j, take, short_rows);
-            const int splits = splits_of(y), parts = class_of(y) == which ? parts_of(y, splits) : 0;
-            x = y;
+            x = share<kRows, kKeys>(a, first + j, take, short_rows);
+            const int splits = splits_of(x), parts = x.row_tiles * a.kv_heads * splits;
             b = first + j;
             if (at < parts) break;
             at -= parts;
@@ -216,37 +188,12 @@ __device__ __forceinline__ bool find_item_of(const AttnArgs &a, int take, int sh
     return true;
 }
 
-template <bool kTree, bool kSplit, int kRows, int kKeys>
+template <int kRows, int kKeys>
 __device__ __forceinline__ bool find_item(const AttnArgs &a, int take, int short_rows, int target, int min_chunk,
                                           int min_tiles, int max_splits, int index, int grid, Item &it) {
     return a.num_requests <= 64
-               ? find_item_of<kTree, kSplit, kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
-               : find_item_of<kTree, kSplit, kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
-}
-
-// One row's mask over its request's new tokens, which a token of a tree sees by.
-struct TreeRow {
-    const uint32_t *words;
-    int count, n;  // words, none for a row past the last; new tokens
-
-    // Bits m .. m + 31, those of tokens that there are not being 0; m is the same for every lane.
-    __device__ __forceinline__ uint32_t bits(int m) const {
-        const int left = n - m, w = m >> 5;
-        if (left <= 0 || m <= -32) return 0;
-        const uint32_t lo = (unsigned)w < (unsigned)count ? words[w] : 0, hi = (unsigned)(w + 1) < (unsigned)count ? words[w + 1] : 0;
-        const uint32_t x = __builtin_amdgcn_alignbit(hi, lo, m & 31);
-        return left < 32 ? x & ((1u << left) - 1) : x;
-    }
-    // How many it sees.
-    __device__ __forceinline__ int seen() const {
-        int sum = 0;
-        for (int m = 0; m < n; m += 32) sum += __popc(bits(m));
-        return sum;
-    }
-};
-
-__device__ __forceinline__ TreeRow tree_row(const AttnArgs &a, const Item &it, int tok, bool valid) {
-    return {a.tree + (int64_t)(it.q0 + (valid ? tok : 0)) * a.tree_words, valid ? a.tree_words : 0, it.n};
+               ? find_item_of<kRows, kKeys, 1>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it)
+               : find_item_of<kRows, kKeys, 8>(a, take, short_rows, target, min_chunk, min_tiles, max_splits, index, grid, it);
 }
 
 // Maximum and sum over the four lanes (l, l ^ 16, l ^ 32, l ^ 48) that hold

@@ -12,10 +12,13 @@
 // row's maximum is a maximum over a lane's registers and two or one lane
 // swaps), the scores leave the first product in the layout in which the second
 // takes its weights, and the order of keys within a product is free.
-#include <type_traits>
-
 #include "kv_attention.h"
 #include "sgmv.h"
+#ifdef SGMV_TREE
+#include <type_traits>
+
+#include "kv_tree_items.h"
+#endif
 
 namespace sgmv {
 
@@ -330,20 +333,32 @@ __device__ __forceinline__ void add_splits(const AttnArgs &a, const Item &it, in
     }
 }
 
-// Item `index` of `grid`. The four LDS regions (kWaveBytes each) are the four
-// waves' own. kOnce: no other row tile reads the same keys, so they are loaded
+#ifdef SGMV_TREE
+template <int kKeys>
+using StreamKind = TreeKind<kStreamRows, kKeys, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits>;
+#else
+template <typename S>
+__device__ __forceinline__ bool find_stream_item(const AttnArgs &a, int take, int index, int grid, Item &it) {
+    return find_item<kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles,
+                                            kStreamMaxSplits, index, grid, it);
+}
+#endif
+
+// One item. The four LDS regions (kWaveBytes each) are the four waves' own. kOnce: no other row tile reads the same keys, so they are loaded
 // past the caches' usual retention: at 64 heads on 8 and 512 requests of 128
 // to 4096 keys 785 -> 720 us, 5.8 -> 6.3 TB/s.
 template <typename T, int D, int U, bool kOnce>
-__device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
-                                            float *slots, unsigned char *lds0, unsigned char *lds1,
-                                            unsigned char *lds2, unsigned char *lds3, StreamSmem &sm) {
+__device__ __forceinline__ void stream_item(const AttnArgs &a, const Item &it, uint32_t *counters, float *slots,
+                                            unsigned char *lds0, unsigned char *lds1, unsigned char *lds2,
+                                            unsigned char *lds3, StreamSmem &sm) {
     using S = Stream<T, D, U>;
     constexpr int NB = S::kBlocks, CH = S::kChunks, NL = S::kLoads;
-    Item it;
-    if (!find_item<kTree, false, kStreamRows, S::kKeys>(a, take, kShortRows, kStreamTarget, kStreamMinChunk, kStreamMinTiles, kStreamMaxSplits, index,
-                                              grid, it)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
+#ifdef SGMV_TREE
+    const int tid = this_thread();
+#else
+    const int tid = threadIdx.x;
+#endif
+    const int lane = tid & 63, wave = tid >> 6, g = lane >> 4, r = lane & 15;
     const int rows = it.n * a.group, row0 = it.row_tile * kStreamRows;
     const int tok_a = row0 / a.group, tok_b = (min(row0 + kStreamRows, rows) - 1) / a.group;
     // First and last position that a row has; a tree's rows are bounded together.
@@ -357,8 +372,15 @@ __device__ __forceinline__ void stream_item(const AttnArgs &a, int take, int ind
     const int my = row0 + r, tok = my / a.group;
     const bool valid = my < rows;
     const int q_head = it.head * a.group + my % a.group;
-    const TreeRow mask = kTree ? tree_row(a, it, tok, valid) : TreeRow{nullptr, 0, 0};
-    const int pos = !valid ? -1 : !kTree ? it.p0 + tok : it.p0 - 1 + (a.window > 0 ? mask.seen() : 0);
+#ifdef SGMV_TREE
+    const TreeRow mask = tree_row(a, it, tok, valid);
+    const int pos = valid ? it.p0 - 1 + (a.window > 0 ? mask.seen() : 0) : -1;
+#else
+    struct {  // a causal row sees by its position alone
+        __device__ __forceinline__ uint32_t bits(int) const { return 0; }
+    } mask;
+    const int pos = valid ? it.p0 + tok : -1;
+#endif
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int last = kTree ? (valid ? it.p0 - 1 : -1) : pos;  // key that is seen for its position
@@ -690,6 +712,9 @@ __device__ __forceinline__ void loads_barrier() {
     lds_barrier();
 }
 
+#ifdef SGMV_TREE
+#include "kv_tree_tile.h"
+#else
 // U as for Stream; kFull: head_dim is D.
 template <int D, int U, bool kFull>
 __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index, int grid, uint32_t *counters,
@@ -699,30 +724,23 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     using S = Stream<bf16_t, D>;  // the LDS layouts of a row
     constexpr int CH = L::kChunks, NL = L::kLoads;
     Item it;
-    if (!find_item<kTree, false, kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
+    if (!find_item<kTileRows, kTileKeys>(a, take, kShortRows, kTileTarget, kTileMinChunk, kTileMinTiles, kTileMaxSplits, index, grid, it)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
     const int rows = it.n * a.group, row0 = it.row_tile * kTileRows;
-    const int pa = kTree ? it.p0 - 1 : it.p0 + row0 / a.group;
-    const int pb = kTree ? it.p0 + it.n - 1 : it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
+    const int pa = it.p0 + row0 / a.group, pb = it.p0 + (min(row0 + kTileRows, rows) - 1) / a.group;
     const TileRun run = tile_run<kTileKeys>(pa, pb, a.window, a.sinks);
     const int splits = run.count > it.size ? (run.count + it.size - 1) / it.size : 1;
     if (it.split >= splits) return;
     const int t0 = it.split * it.size, t1 = min(run.count, t0 + it.size);
 
-    // Trees' tiles of up to 64 rows: two waves have the rows, for the first half of each key tile's keys, and two have
-    // them for the second half.
-    const bool halves = kTree && rows - row0 <= kTileRows / 2;
-    const int row_block = halves ? wave & 1 : wave, key_block = halves ? wave >> 1 : 0;
-    const int wrow = row0 + 32 * row_block;  // this wave's rows; past the last row it only helps loading
+    const int wrow = row0 + 32 * wave;  // this wave's rows; past the last row it only helps loading
     const bool live_wave = wrow < rows;
-    const int wa = kTree ? pa : it.p0 + wrow / a.group, wb = kTree ? pb : it.p0 + (min(wrow + 32, rows) - 1) / a.group;
+    const int wa = it.p0 + wrow / a.group, wb = it.p0 + (min(wrow + 32, rows) - 1) / a.group;
     const int my = wrow + r, tok = my / a.group;
     const bool valid = my < rows;
     const int q_head = it.head * a.group + my % a.group;
-    const TreeRow mask = kTree ? tree_row(a, it, tok, valid) : TreeRow{nullptr, 0, 0};
-    const int pos = !valid ? -1 : !kTree ? it.p0 + tok : it.p0 - 1 + (a.window > 0 ? mask.seen() : 0);
+    const int pos = valid ? it.p0 + tok : -1;
     const int w_lo = a.window > 0 ? pos - a.window + 1 : 0;
-    const int last = kTree ? (valid ? it.p0 - 1 : -1) : pos;  // key that is seen for its position
     const int pa_lo = a.window > 0 ? pa - a.window + 1 : 0, pb_lo = a.window > 0 ? pb - a.window + 1 : 0;
     const int wa_lo = a.window > 0 ? wa - a.window + 1 : 0, wb_lo = a.window > 0 ? wb - a.window + 1 : 0;
     const int head_dim = kFull ? D : a.head_dim, nch = head_dim / 8;
@@ -800,9 +818,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     const auto all_see = [&](int key0) {  // every row sees every key of the tile
         return key0 + kTileKeys - 1 <= pa && (pb_lo <= key0 || key0 + kTileKeys <= a.sinks);
     };
-    // kBlocks: 32-key blocks of a tile that a wave takes, from key_block on.
-    auto step = [&](auto blocks, int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
-        constexpr int kBlocks = decltype(blocks)::value;
+    auto step = [&](int i, unsigned char *kb, unsigned char *vb, unsigned char *k_next, unsigned char *v_next) {
         if (i + 1 < n) {
             if ((i + 1) % 16 == 0) load_pages(i + 1);
             load_tile(i + 1, k_next, v_next);
@@ -822,44 +838,38 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             lds_barrier();
         }
         if (live_wave && key0 <= wb && (key0 + kTileKeys > wa_lo || key0 < a.sinks)) {
-            const int first = kBlocks == 1 ? key_block : 0;  // 32-key block
-            const unsigned char *k_from = kb + first * 32 * CH * 16, *v_from = vb + first * 32 * CH * 16;
-            bf16x8_t kf[kBlocks][L::kSteps];
+            bf16x8_t kf[2][L::kSteps];
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
+            for (int k = 0; k < L::kSteps; ++k) kf[0][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k]);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < L::kSteps; ++k) kf[b][k] = *reinterpret_cast<const bf16x8_t *>(k_from + k_at[k] + b * 32 * CH * 16);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            f32x16_t s[kBlocks];
+            for (int k = 0; k < L::kSteps; ++k) kf[1][k] = *reinterpret_cast<const bf16x8_t *>(kb + k_at[k] + 32 * CH * 16);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x16_t s[2];
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[b][e] = 0.f;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+            for (int k = 0; k < L::kSteps; ++k) s[0] = mfma32(kf[0][k], qf[k], s[0]);
 #pragma unroll
-                for (int k = 0; k < L::kSteps; ++k) s[b] = mfma32(kf[b][k], qf[k], s[b]);
+            for (int k = 0; k < L::kSteps; ++k) s[1] = mfma32(kf[1][k], qf[k], s[1]);
             bf16x8_t vf[2][L::kOut];  // V fragments of two 16-key steps
 #pragma unroll
-            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(v_from + v_at[d], 8 * CH * 16);
+            for (int d = 0; d < L::kOut; ++d) vf[0][d] = read_columns(vb + v_at[d], 8 * CH * 16);
             if (!(key0 + kTileKeys - 1 <= wa && (wb_lo <= key0 || key0 + kTileKeys <= a.sinks))) {
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) {
-                    const int key_b = key0 + 32 * (first + b);
-                    const uint32_t bits = kTree ? mask.bits(key_b - it.p0) >> (4 * h) : 0;
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const int key = key_b + 8 * (e / 4) + 4 * h + e % 4;
-                        bool seen = (key <= last) & ((key >= w_lo) | (key < a.sinks));
-                        if (kTree) seen |= (bits >> (8 * (e / 4) + e % 4) & 1) != 0;
+                        const int key = key0 + 32 * b + 8 * (e / 4) + 4 * h + e % 4;
+                        const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
                         s[b][e] = seen ? s[b][e] : kNone;
                     }
-                }
             }
             float top = kNone;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
             top = swap32_max(top) * c2;
@@ -874,7 +884,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             }
             const float ref = ref_of(m);
 #pragma unroll
-            for (int t = 0; t < 2 * kBlocks; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
+            for (int t = 0; t < 4; ++t) {  // 16 keys: this lane's weight slots are 16 t + 4 h + {0..3, 8..11}
                 float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -886,10 +896,10 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
                 for (int i = 0; i < 4; ++i) split_weights(w[2 * i], w[2 * i + 1], hi[i], lo[i]);
                 const bf16x8_t p = __builtin_bit_cast(bf16x8_t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 const bf16x8_t p_lo = __builtin_bit_cast(bf16x8_t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                if (t + 1 < 2 * kBlocks) {
+                if (t < 3) {
 #pragma unroll
                     for (int d = 0; d < L::kOut; ++d)
-                        vf[(t + 1) & 1][d] = read_columns(v_from + v_at[d] + 16 * (t + 1) * CH * 16, 8 * CH * 16);
+                        vf[(t + 1) & 1][d] = read_columns(vb + v_at[d] + 16 * (t + 1) * CH * 16, 8 * CH * 16);
                 }
 #pragma unroll
                 for (int d = 0; d < L::kOut; ++d) o[d] = mfma32(vf[t & 1][d], p, o[d]);
@@ -905,55 +915,25 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
         load_tile(0, k_even, v_even);
     }
     loads_barrier();
-    const auto steps = [&](auto blocks) {
-        for (int i = 0; i < n; i += 2) {
-            step(blocks, i, k_even, v_even, k_odd, v_odd);
-            if (i + 1 < n) step(blocks, i + 1, k_odd, v_odd, k_even, v_even);
-        }
-    };
-    if (halves)
-        steps(std::integral_constant<int, 1>{});
-    else
-        steps(std::integral_constant<int, 2>{});
-    l = swap32_sum(l);
-    if (halves) {  // the second halves' results, to the waves with the first
-        float *there = reinterpret_cast<float *>(row_block == 0 ? k_even : v_even) + lane;
-        float *more = reinterpret_cast<float *>(k_odd) + row_block * 128 + lane;
-        if (key_block == 1) {
-#pragma unroll
-            for (int d = 0; d < L::kOut; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) there[(16 * d + e) * 64] = o[d][e];
-            more[0] = m;
-            more[64] = l;
-        }
-        lds_barrier();
-        if (key_block == 0) {
-            const float m2 = more[0], top = fmaxf(m, m2);
-            const float keep = exp2_fast(m - ref_of(top)), keep2 = exp2_fast(m2 - ref_of(top));
-            m = top;
-            l = l * keep + more[64] * keep2;
-#pragma unroll
-            for (int d = 0; d < L::kOut; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * keep + there[(16 * d + e) * 64] * keep2;
-        }
+    for (int i = 0; i < n; i += 2) {
+        step(i, k_even, v_even, k_odd, v_odd);
+        if (i + 1 < n) step(i + 1, k_odd, v_odd, k_even, v_even);
     }
-    const bool mine = valid && key_block == 0;  // this wave has its rows' results
+    l = swap32_sum(l);
     // A sum over a value that is not finite is that value, which was cleared, or met a weight's zero low part.
     bool odd = sm.odd != 0;
 #pragma unroll
     for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) odd |= o[d][e] != o[d][e];
-    if (__any(odd && mine && l == l)) {
+    if (__any(odd && valid && l == l)) {
         f32x16_t x[L::kOut];
 #pragma unroll
         for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[d][e] = 0.f;
         each_nonfinite<bf16_t, kTileKeys>(a, it, run, t0, t1, 1, [&](int key, const bf16_t *value) {
-            const bool seen = ((key <= last) & ((key >= w_lo) | (key < a.sinks))) || (kTree && mask.bits(key - it.p0) & 1);
+            const bool seen = (key <= pos) & ((key >= w_lo) | (key < a.sinks));
             if (!__any(seen)) return;
 #pragma unroll
             for (int d = 0; d < L::kOut; ++d)
@@ -975,10 +955,10 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
 
     const __amdgpu_buffer_rsrc_t part =
         part_rsrc(slots + (int64_t)it.first_slot * L::kSlotFloats, (uint32_t)splits * L::kSlotFloats * 4);
-    if (mine) {
+    if (valid) {
         const int64_t q_row = it.q0 + tok;
         const uint32_t slot = (uint32_t)it.split * L::kSlotFloats * 4;
-        const int row = 32 * row_block + r;
+        const int row = 32 * wave + r;
 #pragma unroll
         for (int d = 0; d < L::kOut; ++d)
 #pragma unroll
@@ -1000,7 +980,7 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
             }
         }
     }
-    if (kTree || splits == 1) return;
+    if (splits == 1) return;
 
     uint32_t *counter = counters + it.first_slot;
     if (!arrive_last(counter, (uint32_t)splits, &sm.flag)) return;
@@ -1008,15 +988,34 @@ __device__ __forceinline__ void tile_item(const AttnArgs &a, int take, int index
     add_splits<bf16_t, D, kTileRows, kTileMaxSplits, 4>(a, it, splits, row0, min(kTileRows, rows - row0), part, region, sm);
     if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+#endif
 
 template <typename T, int D, int U, bool kOnce>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void stream_kernel(AttnArgs a, uint32_t *counters, float *slots) {
     using S = Stream<T, D, U>;
     __shared__ __align__(16) unsigned char lds[kWaves][S::kWaveBytes];
     __shared__ StreamSmem sm;
-    stream_item<T, D, U, kOnce>(a, kTakeAll, blockIdx.x, gridDim.x, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
+#ifdef SGMV_TREE
+    one_item<StreamKind<S::kKeys>>(a, blockIdx.x, [&](const Item &it) {
+        stream_item<T, D, U, kOnce>(a, it, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
+    });
+#else
+    Item it;
+    if (find_stream_item<S>(a, kTakeAll, blockIdx.x, gridDim.x, it))
+        stream_item<T, D, U, kOnce>(a, it, counters, slots, lds[0], lds[1], lds[2], lds[3], sm);
+#endif
 }
 
+#ifdef SGMV_TREE
+template <int D, int U, bool kFull>
+__global__ __launch_bounds__(kThreads, 2) void tree_tile_kernel(AttnArgs a, float *slots) {
+    __shared__ __align__(16) unsigned char k_even[Tile<D>::kBytes], v_even[Tile<D>::kBytes], k_odd[Tile<D>::kBytes], v_odd[Tile<D>::kBytes];
+    __shared__ StreamSmem sm;
+    one_item<TileKind>(a, blockIdx.x, [&](const Item &it) {
+        tree_tile_item<D, U, kFull>(a, it, slots, k_even, v_even, k_odd, v_odd, sm);
+    });
+}
+#else
 // Workgroups below `tiles` take the tile items, the others the streaming
 // items, each with counters and slots of its own: in a batch of both, the
 // ones compute while the others read.
@@ -1028,13 +1027,15 @@ __global__ __launch_bounds__(kThreads, 2) void tile_kernel(AttnArgs a, int tiles
     __shared__ __align__(16) unsigned char k_even[kBytes], v_even[kBytes], k_odd[kBytes], v_odd[kBytes];
     __shared__ StreamSmem sm;
     const int index = blockIdx.x;
+    Item it;
     if (index < tiles)
         tile_item<D, U, kFull>(a, gridDim.x == (unsigned)tiles ? kTakeAll : kTakeLong, index, tiles, counters, slots,
                             k_even, v_even, k_odd, v_odd, sm);
-    else
-        stream_item<bf16_t, D, U, true>(a, kTakeShort, index - tiles, gridDim.x - tiles, counters + kMostSplits,
-                               slots + (int64_t)kMostSplits * Tile<D>::kSlotFloats, k_even, v_even, k_odd, v_odd, sm);
+    else if (find_stream_item<Stream<bf16_t, D, U>>(a, kTakeShort, index - tiles, gridDim.x - tiles, it))
+        stream_item<bf16_t, D, U, true>(a, it, counters + kMostSplits, slots + (int64_t)kMostSplits * Tile<D>::kSlotFloats,
+                                        k_even, v_even, k_odd, v_odd, sm);
 }
+#endif
 
 // ----------------------------------------------------------------------------
 // Launches and workspace
@@ -1056,6 +1057,8 @@ int64_t most_groups(const AttnArgs &a, int64_t requests, int rows) {
 struct Grid {
     int64_t tiles, streams;
 };
+
+constexpr int kCus = 256;
 
 Grid grid_of(const AttnArgs &a) {
     if (a.dtype != SGMV_BF16) return {0, most_groups(a, a.num_requests, kStreamRows) * a.kv_heads + kStreamTarget};
@@ -1080,109 +1083,6 @@ auto stream_kernel_of(const AttnArgs &a) {
     return once ? stream_kernel<T, 128, 128, true> : stream_kernel<T, 128, 128, false>;
 }
 
-
-#ifdef SGMV_TREE
-// ----------------------------------------------------------------------------
-// Adding up the splits of a tree's groups, in a launch of its own: a group of
-// 128 rows in 32 splits is 2 MB, which the last of its workgroups alone would
-// read at the latency of 16 loads a lane (one request of 25 tokens behind
-// 31000, 64 heads on 8: 106 us in all). Here split k's workgroup adds the k-th
-// part of the group's rows, a wave a row; the workgroups look for their groups
-// as the attention's do.
-// ----------------------------------------------------------------------------
-template <typename T, int D, int kRows, int kKeys, int kMaxSplits>
-__device__ __forceinline__ void join_item(const AttnArgs &a, int take, int target, int min_chunk, int min_tiles, int index,
-                                          const float *slots) {
-    constexpr int kSlot = kRows * D + 2 * kRows, kPer = D / 64, kRegs = (kMaxSplits + 63) / 64, kDeep = 16;
-    Item it;
-    if (!find_item<true, true, kRows, kKeys>(a, take, kShortRows, target, min_chunk, min_tiles, kMaxSplits, index, kMostSplits, it))
-        return;
-    const TileRun run = tile_run<kKeys>(it.p0 - 1, it.p0 + it.n - 1, a.window, a.sinks);
-    const int splits = (run.count + it.size - 1) / it.size;
-    if (it.split >= splits) return;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = it.row_tile * kRows, live = min(kRows, it.n * a.group - row0);
-    const float *part = slots + (int64_t)it.first_slot * kSlot;
-    for (int row = live * it.split / splits + wave; row < live * (it.split + 1) / splits; row += kWaves) {
-        float f[kRegs], l[kRegs], top = kNone, weight = 0.f;
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            const int k = 64 * i + lane;
-            f[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + row] : kNone;
-            l[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + kRows + row] : 0.f;
-            top = fmaxf(top, f[i]);
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            f[i] = exp2_fast(f[i] - ref_of(top));
-            weight += f[i] * l[i];
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) weight += __shfl_xor(weight, o);
-        float sum[kPer];
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) sum[c] = 0.f;
-        const float *from = part + (int64_t)row * D + kPer * lane;
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            for (int k0 = 64 * i; k0 < min(splits, 64 * i + 64); k0 += kDeep) {
-                float x[kDeep][kPer];
-#pragma unroll
-                for (int j = 0; j < kDeep; ++j)
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) x[j][c] = from[(int64_t)min(k0 + j, splits - 1) * kSlot + c];
-#pragma unroll
-                for (int j = 0; j < kDeep; ++j) {
-                    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[i]), (k0 + j) & 63));
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c)  // a value that is not finite is that value under any weight
-                        sum[c] += k0 + j >= splits ? 0.f : is_finite(x[j][c]) ? x[j][c] * w : x[j][c];
-                }
-            }
-        }
-        const int at = row0 + row, head = it.head * a.group + at % a.group, col = kPer * lane;
-        const int64_t q_row = it.q0 + at / a.group;
-        const float inv = weight > 0.f || weight != weight ? 1.f / weight : 0.f;
-        if (col < a.head_dim) {
-            T *dst = static_cast<T *>(a.out) + q_row * a.out_stride + (int64_t)head * a.head_dim + col;
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-                if constexpr (sizeof(T) == 2)
-                    dst[c].bits = __builtin_bit_cast(uint16_t, (__bf16)(sum[c] * inv));
-                else
-                    dst[c] = sum[c] * inv;
-            }
-        }
-        if (a.lse && lane == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
-    }
-}
-
-// Workgroups below `tiles` (0 or kMostSplits) join the tile kernel's groups, the others the streamed ones.
-template <typename T, int D, int U>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, int tiles, int take_tiles, const float *slots) {
-    const int index = blockIdx.x;
-    if constexpr (sizeof(T) == 2) {
-        if (index < tiles) {
-            join_item<T, D, kTileRows, kTileKeys, kTileMaxSplits>(a, take_tiles, kTileTarget, kTileMinChunk, kTileMinTiles, index, slots);
-            return;
-        }
-    }
-    const float *mine = slots + (tiles > 0 ? (int64_t)kMostSplits * Tile<D>::kSlotFloats : 0);
-    join_item<T, D, kStreamRows, Stream<T, D, U>::kKeys, kStreamMaxSplits>(a, tiles > 0 ? kTakeShort : kTakeAll, kStreamTarget,
-                                                                         kStreamMinChunk, kStreamMinTiles, index - tiles, mine);
-}
-
-// The most key tiles that a group of the call can have.
-int64_t most_tiles(const AttnArgs &a, int keys) {
-    const int64_t all = (((int64_t)a.max_blocks << a.page_shift) + keys - 1) / keys;
-    if (a.window == 0) return all;
-    const int64_t seen = ((int64_t)a.window + a.max_q_len) / keys + 2 + ((int64_t)a.sinks + keys - 1) / keys;
-    return seen < all ? seen : all;
-}
-#endif
-
 }  // namespace
 
 #ifndef SGMV_TREE
@@ -1193,22 +1093,12 @@ size_t attention_workspace_bytes(int head_dim, int dtype) {
     return kCounterBytes + (size_t)kMostSplits * (stream + tile) * sizeof(float);
 }
 
-#endif
-
-#ifdef SGMV_TREE
-int64_t tree_attention_workgroups(const AttnArgs &a) {
-#else
 int64_t attention_workgroups(const AttnArgs &a) {
-#endif
     const Grid g = grid_of(a);
     return g.tiles + g.streams;
 }
 
-#ifdef SGMV_TREE
-hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t st) {
-#else
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-#endif
     uint32_t *counters = static_cast<uint32_t *>(a.workspace);
     float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
     const Grid g = grid_of(a);
@@ -1224,21 +1114,58 @@ hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
                                                 : tile_kernel<128, 128, false>;
         hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a, (int)g.tiles, counters, slots);
     }
-#ifdef SGMV_TREE
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const bool bf16 = a.dtype == SGMV_BF16;
-    const bool tiles = g.tiles > 0 && most_tiles(a, kTileKeys) >= kTileMinTiles;
-    const bool streams = (g.tiles == 0 || g.streams > 0) && most_tiles(a, bf16 ? 32 : 16) >= kStreamMinTiles;
-    if (tiles || streams) {
-        const int tile_groups = g.tiles > 0 ? kMostSplits : 0;
-        const auto join = bf16 ? (a.head_dim <= 64 ? join_kernel<bf16_t, 64, 64> : join_kernel<bf16_t, 128, 128>)
-                               : (a.head_dim <= 64 ? join_kernel<float, 64, 64> : join_kernel<float, 128, 128>);
-        hipLaunchKernelGGL(join, dim3(tile_groups + (streams ? kMostSplits : 0)), dim3(kThreads), 0, st, a, tile_groups,
-                           g.streams == 0 ? kTakeAll : kTakeLong, slots);
-    }
-#endif
     return hipGetLastError();
 }
+
+#else
+
+namespace {
+
+// Whether a call is streamed: fp32 is, and bf16 whose requests have few rows. Streaming takes 16 rows against the keys,
+// and splits finer. Up to 32 rows it is as good or better where the GPU has no more groups than it runs at once, 64 heads on
+// 8: 4 requests of 4 tokens over 2000 keys 18 us against 24, 64 over 127 to 4095 122 against 125; with many the second
+// pass over the keys costs more: 64 requests of 32 tokens over up to 2047, 32 heads of their own, 249 against 217.
+bool is_streamed(const AttnArgs &a) {
+    const int64_t rows = (int64_t)a.max_q_len * a.group, groups = (int64_t)a.num_requests * a.kv_heads;
+    return a.dtype != SGMV_BF16 || rows <= (groups <= 2 * kTileTarget ? 2 * kStreamRows : kStreamRows);
+}
+
+// Adds up the splits of the launch before, if it can have any.
+template <typename T, typename Kind>
+void launch_join(const AttnArgs &a, const float *slots, hipStream_t st) {
+    if (most_tiles(a, Kind::kKeys) < Kind::kMinTiles) return;
+    const auto kernel = a.head_dim <= 64 ? join_kernel<T, 64, Kind> : join_kernel<T, 128, Kind>;
+    hipLaunchKernelGGL(kernel, dim3(3 * kCus), dim3(kThreads), 0, st, a, slots);  // a group in parts has 683 at most
+}
+
+}  // namespace
+
+int64_t tree_attention_workgroups(const AttnArgs &a) {
+    const bool streamed = is_streamed(a);
+    return most_groups(a, a.num_requests, streamed ? kStreamRows : kTileRows) * a.kv_heads + (streamed ? kStreamTarget : kTileTarget);
+}
+
+hipError_t launch_tree_attention(const AttnArgs &a, hipStream_t st) {
+    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kCounterBytes);
+    const dim3 grid((unsigned)tree_attention_workgroups(a));
+    if (a.dtype != SGMV_BF16) {
+        hipLaunchKernelGGL(stream_kernel_of<float>(a), grid, dim3(kThreads), 0, st, a, (uint32_t *)nullptr, slots);
+        launch_join<float, StreamKind<16>>(a, slots, st);
+    } else if (is_streamed(a)) {
+        hipLaunchKernelGGL(stream_kernel_of<bf16_t>(a), grid, dim3(kThreads), 0, st, a, (uint32_t *)nullptr, slots);
+        launch_join<bf16_t, StreamKind<32>>(a, slots, st);
+    } else {
+        const auto kernel = a.head_dim == 64    ? tree_tile_kernel<64, 64, true>
+                            : a.head_dim == 128 ? tree_tile_kernel<128, 128, true>
+                            : a.head_dim < 64   ? tree_tile_kernel<64, 64, false>
+                            : a.head_dim <= 96  ? tree_tile_kernel<128, 96, false>
+                                                : tree_tile_kernel<128, 128, false>;
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, a, slots);
+        launch_join<bf16_t, TileKind>(a, slots, st);
+    }
+    return hipGetLastError();
+}
+
+#endif
 
 }  // namespace sgmv

@@ -10,7 +10,8 @@
 // What bounds it: latency. Up to kOneBlock choices one workgroup does it all;
 // beyond, workgroups count a run of choices each (to the workspace), and a
 // second launch, in which every workgroup adds the others' counts up for
-// itself, places them.
+// itself, places them. A wave keeps what it found out about its choices, eight
+// steps of 64 at most, from counting them to placing them.
 #include "route_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"
@@ -21,15 +22,16 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kOneBlock = 4096;   // choices that one workgroup sorts by itself
+constexpr int kSteps = 8;                       // of 64 choices that a wave keeps
+constexpr int kOneBlock = kSteps * kThreads;    // choices that one workgroup sorts by itself
 constexpr int kMaxBlocks = 64;
-constexpr int kRun = 1024;        // choices per workgroup, at least, where there are several
+constexpr int kRun = kThreads;    // choices per workgroup, at least, where there are several
 
 struct Split {
     int blocks, run;  // run: choices per workgroup, a multiple of kThreads
 };
 Split split_of(int n) {
-    if (n <= kOneBlock) return {1, kOneBlock};
+    if (n <= kOneBlock) return {1, (n + kThreads - 1) / kThreads * kThreads};
     int run = (n + kMaxBlocks - 1) / kMaxBlocks;
     run = (run < kRun ? kRun : run + kThreads - 1) / kThreads * kThreads;
     return {(n + run - 1) / run, run};
@@ -60,26 +62,45 @@ __device__ __forceinline__ void wave_lds_order() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// Calls f(key, index, lanes with this key) for this wave's part [lo, hi) of the run, 64 choices at a time, in order.
-template <typename F>
-__device__ __forceinline__ void each_step(const SortArgs &a, int lo, int hi, int bits, F f) {
+// 64 choices: this lane's key (-1: none), its rank among the lanes with the same key, and their number where it is their
+// first (0 elsewhere).
+struct Step {
+    int key, rank, count;
+};
+__device__ __forceinline__ Step step_of(const SortArgs &a, int i, int end, int bits) {
+    const int key = key_of(a, i, end);
+    const unsigned long long who = same_key(key, bits);
+    const int rank = (int)__popcll(who & lanes_below(threadIdx.x & 63));
+    return {key, rank, key >= 0 && rank == 0 ? (int)__popcll(who) : 0};
+}
+
+// Calls f(step, index) for this wave's part [lo, hi) of the run, 64 choices at a time, in order. With kKeep the first
+// kSteps steps are left in, or taken from, `kept`.
+enum Kept { kFill, kUse };
+template <Kept kKept, typename F>
+__device__ __forceinline__ void each_step(const SortArgs &a, int lo, int hi, int bits, Step (&kept)[kSteps], F f) {
     const int lane = threadIdx.x & 63;
-    for (int i0 = lo; i0 < hi; i0 += 64) {
-        const int key = key_of(a, i0 + lane, hi);
-        f(key, i0 + lane, same_key(key, bits));
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int i0 = lo + 64 * s;
+        if (i0 >= hi) break;
+        if constexpr (kKept == kFill) kept[s] = step_of(a, i0 + lane, hi, bits);
+        f(kept[s], i0 + lane);
     }
+    for (int i0 = lo + 64 * kSteps; i0 < hi; i0 += 64) f(step_of(a, i0 + lane, hi, bits), i0 + lane);
 }
 
 // Counts of one run, to the workspace.
 template <int kBins>
 __global__ __launch_bounds__(kThreads) void count_kernel(SortArgs a, int run, int bits) {
     __shared__ uint32_t s_count[kBins];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, wave = tid >> 6;
     for (int k = tid; k < a.num_adapters; k += kThreads) s_count[k] = 0;
     __syncthreads();
     const int part = run / kWaves, lo = min(blockIdx.x * run + wave * part, (unsigned)a.n), hi = min(lo + part, a.n);
-    each_step(a, lo, hi, bits, [&](int key, int, unsigned long long who) {
-        if (key >= 0 && (who & lanes_below(lane)) == 0) atomicAdd(&s_count[key], (uint32_t)__popcll(who));  // a sum: in any order
+    Step kept[kSteps];
+    each_step<kFill>(a, lo, hi, bits, kept, [&](const Step &s, int) {
+        if (s.count > 0) atomicAdd(&s_count[s.key], (uint32_t)s.count);  // a sum: in any order
     });
     __syncthreads();
     for (int k = tid; k < a.num_adapters; k += kThreads) a.counts[(int64_t)blockIdx.x * a.num_adapters + k] = s_count[k];
@@ -113,6 +134,8 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair (*s_wave)[kWaves], int r
     return v;
 }
 
+constexpr int kAtOnce = 16;  // workgroups' counts that are read together
+
 // kOne: the only workgroup, which counts for itself.
 template <int kBins, bool kOne>
 __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, int blocks, int bits) {
@@ -122,8 +145,9 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, in
     for (int k = lane; k < P; k += 64) s_at[wave][k] = 0;
     wave_lds_order();
     const int part = run / kWaves, lo = min(blockIdx.x * run + wave * part, (unsigned)a.n), hi = min(lo + part, a.n);
-    each_step(a, lo, hi, bits, [&](int key, int, unsigned long long who) {
-        if (key >= 0 && (who & lanes_below(lane)) == 0) s_at[wave][key] += __popcll(who);
+    Step kept[kSteps];
+    each_step<kFill>(a, lo, hi, bits, kept, [&](const Step &s, int) {
+        if (s.count > 0) s_at[wave][s.key] += s.count;
         wave_lds_order();
     });
     __syncthreads();
@@ -143,10 +167,16 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, in
             if constexpr (kOne) {
                 all = sum;
             } else {
-                for (int b = 0; b < blocks; ++b) {
-                    const uint32_t c = a.counts[(int64_t)b * P + k];
-                    before += b < (int)blockIdx.x ? c : 0;
-                    all += c;
+                for (int b0 = 0; b0 < blocks; b0 += kAtOnce) {
+                    uint32_t c[kAtOnce];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) c[i] = a.counts[(int64_t)min(b0 + i, blocks - 1) * P + k];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        const uint32_t x = b0 + i < blocks ? c[i] : 0;
+                        before += b0 + i < (int)blockIdx.x ? x : 0;
+                        all += x;
+                    }
                 }
             }
         }
@@ -173,18 +203,18 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, in
     }
     __syncthreads();
 
-    each_step(a, lo, hi, bits, [&](int key, int i, unsigned long long who) {
+    each_step<kUse>(a, lo, hi, bits, kept, [&](const Step &s, int i) {
         if (i < hi) {
             int row = -1;
-            if (key >= 0) {
-                row = s_at[wave][key] + __popcll(who & lanes_below(lane));
+            if (s.key >= 0) {
+                row = s_at[wave][s.key] + s.rank;
                 a.order[row] = i;
             }
             a.place[i] = row;
             if (i >= done.x) a.order[i] = -1;
         }
         wave_lds_order();
-        if (key >= 0 && (who & lanes_below(lane)) == 0) s_at[wave][key] += __popcll(who);
+        if (s.count > 0) s_at[wave][s.key] += s.count;
         wave_lds_order();
     });
 }
@@ -214,6 +244,8 @@ hipError_t launch_sort_tokens(const SortArgs &a, hipStream_t st) {
         launch<256>(a, s, bits, st);
     else if (a.num_adapters <= 1024)
         launch<1024>(a, s, bits, st);
+    else if (a.num_adapters <= 2048)
+        launch<2048>(a, s, bits, st);
     else
         launch<SGMV_MAX_SORTED_ADAPTERS>(a, s, bits, st);
     return hipGetLastError();
