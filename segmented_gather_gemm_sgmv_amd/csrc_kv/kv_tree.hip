@@ -77,18 +77,20 @@ __global__ __launch_bounds__(kThreads) void tree_accept_kernel(AcceptArgs a) {
     int q0, n;
     rows_of(a.q_start, a.num_requests, a.T, b, q0, n);
     int accepted = 0, next = -1;
-    if (b < a.num_requests && n > 0 && a.slot[q0] >= 0) {
+    if (b < a.num_requests && n > 0) {
         Walk &t = s_walk[wave];
         const int size = min(n, kMaxTree);
+        const bool served = a.slot[q0] >= 0;  // with its tree in one go
         for (int i = lane; i < size; i += 64) {
-            t.parent[i] = a.parent[q0 + i];
-            t.token[i] = a.token[q0 + i];
-            t.target[i] = a.target[q0 + i];
+            const int parent = a.parent[q0 + i], token = a.token[q0 + i], target = a.target[q0 + i];
+            t.parent[i] = parent;
+            t.token[i] = token;
+            t.target[i] = target;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
         __builtin_amdgcn_wave_barrier();
         int cur = 0;
-        while (true) {  // cur grows
+        while (served) {  // cur grows
             next = t.target[cur];
             if (lane == 0) a.path[q0 + accepted] = cur;
             ++accepted;

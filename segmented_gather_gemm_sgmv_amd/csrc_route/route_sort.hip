@@ -25,7 +25,12 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kSteps = 8;                       // of 64 choices that a wave keeps
 constexpr int kOneBlock = kSteps * kThreads;    // choices that one workgroup sorts by itself
 constexpr int kMaxBlocks = 64;
-constexpr int kRun = kThreads;    // choices per workgroup, at least, where there are several
+constexpr int kRun = 2 * kThreads;  // choices per workgroup, at least, where there are several
+
+constexpr int kBinsEach = 4;  // neighbouring adapters that a thread adds up: 16 bytes of every workgroup's counts
+
+// Counts of one workgroup in the workspace.
+__host__ __device__ __forceinline__ int stride_of(int num_adapters) { return (num_adapters + kBinsEach - 1) / kBinsEach * kBinsEach; }
 
 struct Split {
     int blocks, run;  // run: choices per workgroup, a multiple of kThreads
@@ -103,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void count_kernel(SortArgs a, int run, in
         if (s.count > 0) atomicAdd(&s_count[s.key], (uint32_t)s.count);  // a sum: in any order
     });
     __syncthreads();
-    for (int k = tid; k < a.num_adapters; k += kThreads) a.counts[(int64_t)blockIdx.x * a.num_adapters + k] = s_count[k];
+    for (int k = tid; k < a.num_adapters; k += kThreads) a.counts[(int64_t)blockIdx.x * stride_of(a.num_adapters) + k] = s_count[k];
 }
 
 // Inclusive sums of x and y over the workgroup's threads; adds them up with `base` (in, out: for the next round).
@@ -152,45 +157,61 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, in
     });
     __syncthreads();
 
-    // Rows before each adapter, and the segments, kThreads adapters a round.
+    // Rows before each adapter, and the segments, kBinsEach * kThreads adapters a round.
     Pair done = {0, 0};
-    const int rounds = (P + kThreads - 1) / kThreads;
+    const int rounds = (P + kBinsEach * kThreads - 1) / (kBinsEach * kThreads);
     for (int r = 0; r < rounds; ++r) {
-        const int k = r * kThreads + tid;
-        uint32_t here[kWaves], sum = 0, before = 0, all = 0;
-        if (k < P) {
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                here[w] = sum;
-                sum += s_at[w][k];
-            }
+        const int k0 = (r * kThreads + tid) * kBinsEach, bins = min(P - k0, kBinsEach);
+        uint32_t before[kBinsEach] = {0, 0, 0, 0}, all[kBinsEach] = {0, 0, 0, 0};
+        if (bins > 0) {
             if constexpr (kOne) {
-                all = sum;
-            } else {
-                for (int b0 = 0; b0 < blocks; b0 += kAtOnce) {
-                    uint32_t c[kAtOnce];
 #pragma unroll
-                    for (int i = 0; i < kAtOnce; ++i) c[i] = a.counts[(int64_t)min(b0 + i, blocks - 1) * P + k];
+                for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+                    for (int c = 0; c < kBinsEach; ++c) all[c] += s_at[w][k0 + c];
+            } else {
+                const uint32_t *counts = a.counts + k0;
+                for (int b0 = 0; b0 < blocks; b0 += kAtOnce) {
+                    uint4 x[kAtOnce];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) x[i] = ld16(counts + (int64_t)min(b0 + i, blocks - 1) * stride_of(P));
 #pragma unroll
                     for (int i = 0; i < kAtOnce; ++i) {
-                        const uint32_t x = b0 + i < blocks ? c[i] : 0;
-                        before += b0 + i < (int)blockIdx.x ? x : 0;
-                        all += x;
+                        const uint32_t y[kBinsEach] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int c = 0; c < kBinsEach; ++c) {
+                            before[c] += b0 + i < (int)blockIdx.x ? y[c] : 0;
+                            all[c] += b0 + i < blocks ? y[c] : 0;
+                        }
                     }
                 }
             }
         }
-        Pair total;
-        const Pair to = block_scan(Pair{(int)all, all > 0 ? 1 : 0}, s_wave, r, total);
-        const int start = done.x + to.x - (int)all;
-        if (k < P) {
+        Pair mine = {0, 0};
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) s_at[w][k] = start + before + here[w];
-            if (blockIdx.x == 0 && all > 0) {
-                const int s = done.y + to.y - 1;
-                a.seg_start[s] = start;
-                a.seg_adapter[s] = k;
+        for (int c = 0; c < kBinsEach; ++c) {
+            if (c >= bins) all[c] = 0;
+            mine.x += all[c];
+            mine.y += all[c] > 0;
+        }
+        Pair total;
+        const Pair to = block_scan(mine, s_wave, r, total);
+        int start = done.x + to.x - mine.x, seg = done.y + to.y - mine.y;
+#pragma unroll
+        for (int c = 0; c < kBinsEach; ++c) {
+            if (c >= bins) continue;
+            uint32_t at = start + before[c];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const uint32_t here = s_at[w][k0 + c];
+                s_at[w][k0 + c] = at;
+                at += here;
             }
+            if (blockIdx.x == 0 && all[c] > 0) {
+                a.seg_start[seg] = start;
+                a.seg_adapter[seg++] = k0 + c;
+            }
+            start += all[c];
         }
         done.x += total.x;
         done.y += total.y;
@@ -233,7 +254,7 @@ void launch(const SortArgs &a, Split s, int bits, hipStream_t st) {
 
 size_t sort_workspace_bytes(int n, int num_adapters) {
     const Split s = split_of(n);
-    return s.blocks == 1 ? 0 : (size_t)s.blocks * num_adapters * sizeof(uint32_t);
+    return s.blocks == 1 ? 0 : (size_t)s.blocks * stride_of(num_adapters) * sizeof(uint32_t);
 }
 
 hipError_t launch_sort_tokens(const SortArgs &a, hipStream_t st) {
