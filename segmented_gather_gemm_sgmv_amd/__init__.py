@@ -748,7 +748,7 @@ def sgmv_sort_tokens(choice: torch.Tensor, num_adapters: int, seg_start: torch.T
     one choice per token order is their `rows`."""
     ws = workspace_buf
     if ws is None and choice.dim() == 2:
-        need = int(lib.sgmv_sort_tokens_workspace_bytes(choice.shape[0], choice.shape[1], num_adapters))
+        need = int(lib.sgmv_sort_tokens_workspace_bytes(choice.shape[0], choice.shape[1], int(num_adapters)))
         if need and choice.is_cuda:  # the call's own, so that calls on other streams and replays have nothing to do with it
             with torch.cuda.stream(None if stream is None else _torch_stream(choice.device, stream)):
                 ws = torch.empty(need, dtype=torch.uint8, device=choice.device)

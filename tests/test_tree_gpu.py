@@ -151,6 +151,26 @@ def test_tree_attention(dev, dtype, sizes, ctx, hq, hk, d, page):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("B,most,ctx,hq,hk,d", [
+    (64, 6, 150, 4, 1, 64),       # as many requests as a wave has lanes; up to 24 rows, streamed in bf16
+    (65, 9, 90, 2, 2, 64),        # two per lane
+    (70, 20, 60, 16, 16, 8),      # more groups than the GPU runs at once, few rows each
+    (600, 3, 40, 2, 1, 64),       # more than eight per lane
+    (130, 40, 300, 4, 2, 128)])
+def test_many_requests(dev, dtype, B, most, ctx, hq, hk, d):
+    """Items found among many requests, the longest first; every tenth request without tokens, some without a cache."""
+    rng = np.random.default_rng(B)
+    sizes = [int(n) if b % 10 else 0 for b, n in enumerate(rng.integers(1, most + 1, B))]
+    check(dev, rng, sizes, [int(c) if b % 7 else 0 for b, c in enumerate(rng.integers(0, ctx + 1, B))], hq, hk, d, dtype, 16)
+
+
+@pytest.mark.parametrize("sizes,ctx", [([6, 3], [3000, 700]), ([30, 2, 9], [2500, 1, 4000])])
+def test_splits_beside_whole_groups(dev, sizes, ctx):
+    check(dev, np.random.default_rng(sum(ctx)), sizes, ctx, 4, 1, 64, BF16, 16)
+    check(dev, np.random.default_rng(sum(ctx)), sizes, ctx, 4, 1, 64, F32, 16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("sizes,ctx,group", [([20, 7], [40, 0], 2), ([60, 90], [0, 100], 1), ([33], [31], 4)])
 def test_any_mask(dev, dtype, sizes, ctx, group):
     """Bits of tokens behind the row's own and of tokens that there are not, and rows without any."""
