@@ -5,7 +5,8 @@
 //
 // What bounds them: latency. A step's trees are a few KB; each kernel is a
 // chain of dependent reads, so a request's chain is walked in LDS or registers
-// and requests go side by side, a workgroup or a wave each.
+// and requests go side by side, a workgroup or a wave each. An empty kernel
+// takes 1.6 us.
 #include "kv_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"
@@ -29,7 +30,8 @@ __device__ __forceinline__ void rows_of(const int32_t *q_start, int B, int T, in
 // Positions and masks. A token's ancestors have falling indices, so its walk
 // up the tree (parents in LDS) meets the words of its mask from the last to
 // the first, and each is written once.
-// Measured: see the launch below.
+// Measured (kernel alone): 64 trees of 26 to 64 tokens 2.8 us; 512 of up to 256
+// with 8 words each, 2.7 MB, 4.3 us.
 // ----------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void tree_tables_kernel(TreeTablesArgs a) {
     __shared__ int s_parent[kMaxTree];
@@ -64,6 +66,10 @@ __global__ __launch_bounds__(kThreads) void tree_tables_kernel(TreeTablesArgs a)
 // Acceptance. A wave takes one request: its tree is read once to LDS, then each
 // step looks for the first child of the present token that holds the model's
 // own next one, 64 candidates at a time (children come after their parents).
+// Giving pages back takes sums over all requests, which here would wait for
+// every wave, and is a launch of its own.
+// Measured (kernel alone): 64 requests of 26 to 64 tokens 4.3 us and 2.7 for
+// the pages, 256 of up to 128 tokens 5.2 and 3.2.
 // ----------------------------------------------------------------------------
 struct Walk {
     int parent[kMaxTree], token[kMaxTree], target[kMaxTree];
@@ -184,6 +190,9 @@ __global__ __launch_bounds__(kThreads) void give_back_kernel(AcceptArgs a) {
 // in order: since path grows, path[d] >= d, a row is read before it is
 // overwritten, and lanes have no bytes in common, so nothing else is waited
 // for. Up to kDeep rows are in flight.
+// Measured (kernel alone): 64 requests, one layer of 32 heads of 128, 4.4 us;
+// 256 requests, eight layers of 8 heads, some 49 MB read and written, 12.0 us
+// (4.1 TB/s; a copy reaches 4.7).
 // ----------------------------------------------------------------------------
 constexpr int kDeep = 4;
 

@@ -1,6 +1,28 @@
 // The tile kernel of trees, and the launch that adds up split groups: part of
 // kv_attention.hip where it is compiled for trees (it has the LDS layouts, the
 // products and the launches).
+//
+// The tile kernel is the causal one's (128 rows on four waves, tiles of 64 keys
+// in two buffers) with three differences. Its rows see the cached keys alike,
+// so that a tile is bounded by the request, not by the row, and only the last
+// tiles look at masks. A row tile of up to 64 rows, which a request with heads
+// of its own has, would leave two waves idle: they take the other half of each
+// tile's keys, and the halves' results meet in LDS. And a split group's parts
+// are added up by another launch.
+//
+// What bounds it: with many rows the matrix cores and the softmax beside them,
+// at the clock that the power limit leaves (128 trees of 64 tokens behind 127
+// to 4095, 64 heads on 8: 955 us, 636 TFLOP/s, with the weights' second half
+// 960; of the 35 tiles of a group the last two hold the tree, of which a token
+// sees a tenth). With few rows HBM: 64 trees of 17 to 64 tokens behind up to
+// 2047, 32 heads of their own, 239 us, 5.05 TB/s. There an item's loop runs at
+// HBM's rate, 2.4 us a tile on two workgroups a CU, and its begin (finding it,
+// pages, first tile) and end, 12 us of 53, are what is left.
+// Tried for few rows, 64 requests of 64 rows and 1000 keys, 254 us as it is: K
+// and V waited for separately and buffers filled as soon as they are read, 254;
+// two waves of 32 rows and tiles of 32 keys, four workgroups a CU, 241, but 170
+// for 139 where there are 512 groups, not 2048; workgroups that stay and take
+// every 512th item, 264; three workgroups a CU, registers spilled.
 
 // Every wave's loads to LDS have landed, and its reads and writes of LDS are done.
 __device__ __forceinline__ void landed_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -323,10 +345,11 @@ __device__ __forceinline__ void tree_tile_item(const AttnArgs &a, const Item &it
 // ----------------------------------------------------------------------------
 // Adding up the splits of a tree's groups, in a launch of its own: a group of
 // 128 rows in 32 splits is 2 MB, which the last of its workgroups alone would
-// read at the latency of 16 loads a lane (one request of 25 tokens behind
-// 31000, 64 heads on 8: 106 us in all). Here split k's workgroup adds the k-th
+// read at the latency of 16 loads a lane. Here split k's workgroup adds the k-th
 // part of the group's rows, a wave a row; the workgroups look for their groups
-// as the attention's do.
+// as the attention's do. One request of 25 tokens behind 31000, 64 heads on 8:
+// 67 us in all, 9.9 of it here (31 MB), and 104 with the last workgroup's. A
+// launch without splits costs 4.8 us, where the table of pages allows any.
 // ----------------------------------------------------------------------------
 template <typename T, int D, typename Kind>
 __device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, const float *slots) {

