@@ -87,6 +87,36 @@ def test_sort_of_one_choice_is_the_host_grouping(dev, T):
     assert torch.equal(by_host, by_device)
 
 
+def test_tokens_without_an_adapter_are_left_by_the_gathered_call(dev):
+    """Some tokens have no adapter: order, with its -1 past the last row, is still what the gathered calls take."""
+    rng = np.random.default_rng(12)
+    T, P = 400, 6
+    choice = rng.integers(-1, P, (T, 1))
+    (start, adapter, order, _), _ = run_sort(dev, choice, P)
+    A, B = (torch.randn(P, 16, 64, device=dev).bfloat16() for _ in range(2))
+    X, Y = (torch.randn(T, 64, device=dev).bfloat16() for _ in range(2))
+    got = sg.sgmv_fused_gather(Y.clone(), X, order, sg.sgmv_pool_pointers(A), sg.sgmv_pool_pointers(B), start, adapter, 16, 16.0)
+    k = torch.from_numpy(np.maximum(choice[:, 0], 0)).to(dev)
+    v = (X.double()[:, None] * A.double()[k]).sum(-1)
+    want = Y.double() + torch.where(torch.from_numpy(choice >= 0).to(dev), (v[..., None] * B.double()[k]).sum(1), 0.0)
+    assert torch.equal(got[choice[:, 0] < 0], Y[choice[:, 0] < 0])
+    # fp32 sums of the width and the rank, V in 16 bits (2^-16 of the terms), one rounding
+    tol = U16 * want.abs() * 1.01 + 2.0 ** -15 * (v.abs()[..., None] * B.double()[k].abs()).sum(1)
+    assert bool(((got.double() - want).abs() <= tol).all())
+
+
+def test_one_adapter_twice(dev):
+    """Both of a token's choices may be one adapter: two rows, and both weights."""
+    choice = np.array([[3, 3], [1, 3], [3, 1]])
+    (start, adapter, order, place), want = run_sort(dev, choice, 5)
+    assert np.array_equal(order.cpu().numpy(), want[2]) and adapter.tolist()[:2] == [1, 3] and start.tolist()[:3] == [0, 2, 6]
+    X = torch.randn(3, 16, device=dev)
+    Xs = sg.sgmv_spread_rows(torch.zeros(6, 16, device=dev), X, place)
+    weight = torch.tensor([[1.0, 2.0], [0.5, 0.25], [4.0, 8.0]], device=dev)
+    Y = sg.sgmv_combine_rows(torch.empty_like(X), Xs, place, weight)
+    assert torch.allclose(Y, X * weight.sum(1, keepdim=True), rtol=4 * U32, atol=0)
+
+
 def test_sort_takes_any_values(dev):
     rng = np.random.default_rng(0)
     choice = rng.integers(-2 ** 31, 2 ** 31, (3000, 2))

@@ -264,6 +264,32 @@ def test_repeated_calls_give_the_same_bits(dev):
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
 
+@pytest.mark.parametrize("n", [6, 40])
+def test_a_cache_past_32_bits(dev, n):
+    """Pages whose offsets pass 2^31 elements and 2^32 bytes: attention (streamed and tiled), and the accepted rows' moves."""
+    pages, hk, page, d = 20000, 8, 128, 128          # 5.2 GB of K and of V
+    if torch.cuda.mem_get_info(dev)[0] < 24 << 30:
+        pytest.skip("needs 24 GB of GPU memory")
+    rng = np.random.default_rng(n)
+    small, h = make(dev, rng, [n], [300], hk, hk, d, BF16, page)
+    used = h["block_table"][0, :-(-(300 + n) // page)]
+    K, V = (torch.empty(pages, hk, page, d, dtype=BF16, device=dev) for _ in range(2))
+    where = pages - 1 - np.arange(len(used)) * 7
+    for i, p in enumerate(used):
+        K[where[i]], V[where[i]] = small["K"][p], small["V"][p]
+    table = np.full((1, 5), -1)
+    table[0, :len(used)] = where
+    x = dict(small, K=K, V=V, block_table=ints(table, dev))
+    got, want = attend(x, 0.1, n), attend(small, 0.1, n)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    slot = where[(300 + np.arange(n)) // page].astype(np.int64) * page + (300 + np.arange(n)) % page
+    before = K[slot[3] // page, :, slot[3] % page].clone()
+    path = np.full(n, -1)
+    path[:2] = [0, 3]
+    sg.sgmv_kv_commit(K, V, ints(slot, dev), ints([0, n], dev), ints(path, dev))
+    assert torch.equal(K[slot[1] // page, :, slot[1] % page], before)
+
+
 # -- acceptance ------------------------------------------------------------------------
 def accept_case(rng, sizes, ctx, page, agree, vocabulary=50, refused=(), free=7):
     parents = [ref.random_tree(rng, n) for n in sizes]
