@@ -712,7 +712,8 @@ int sgmv_sort_tokens(const int32_t *choice, int32_t T, int32_t choices, int32_t 
 size_t sgmv_sort_tokens_workspace_bytes(int32_t T, int32_t choices, int32_t num_adapters);
 
 /* Xs[place[t][j]] = X[t]. Rows of Xs that no choice has are left as they were;
- * one that two choices have holds either's. */
+ * one that two choices have (sgmv_sort_tokens gives each its own) holds
+ * either's. Xs must not overlap X. */
 int sgmv_spread_rows(void *Xs, int64_t Xs_stride, int32_t rows, const void *X, int64_t X_stride,
                      const int32_t *place, int32_t T, int32_t choices, int32_t d, int32_t dtype, void *stream);
 
@@ -726,7 +727,9 @@ int sgmv_combine_rows(void *Y, int64_t Y_stride, const void *base, int64_t base_
 /* dYs[place[t][j]] = weight[t][j] * dY[t], and dweight[t][j] = dY[t] .
  * Ys[place[t][j]] (0 for a choice without a row). dYs or dweight may be NULL;
  * without dweight Ys may be NULL, without dYs weight is not read. Rows of dYs
- * that no choice has are left as they were. dYs must not overlap dY or Ys. */
+ * that no choice has are left as they were; one that two choices have holds
+ * either's, which is then not the gradient (the sum of both). dYs must not
+ * overlap dY or Ys. */
 int sgmv_combine_rows_grad(void *dYs, int64_t dYs_stride, float *dweight, const void *dY, int64_t dY_stride,
                            const void *Ys, int64_t Ys_stride, int32_t rows, const int32_t *place,
                            const float *weight, int32_t T, int32_t choices, int32_t d, int32_t dtype,

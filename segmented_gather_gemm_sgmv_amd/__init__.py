@@ -782,8 +782,9 @@ def sgmv_combine_rows_grad(dYs: Optional[torch.Tensor], dweight: Optional[torch.
                            Ys: Optional[torch.Tensor], place: torch.Tensor, weight: Optional[torch.Tensor] = None,
                            stream=None) -> None:
     """Gradients of sgmv_combine_rows: dYs[place[t, j]] = weight[t, j] * dY[t] and
-    dweight[t, j] = dY[t] . Ys[place[t, j]] (fp32). Either may be None. The
-    gradient of base is dY."""
+    dweight[t, j] = dY[t] . Ys[place[t, j]] (fp32). Either may be None. Each
+    choice has a row of its own, as sgmv_sort_tokens gives it. The gradient of
+    base is dY."""
     st = _kv_binding.combine_rows_grad(dYs, dweight, dY, Ys, place, weight, _stream(dY, stream))
     if st:
         raise SGMVError("sgmv_combine_rows_grad", st)
