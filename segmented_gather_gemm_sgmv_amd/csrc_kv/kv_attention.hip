@@ -1058,8 +1058,6 @@ struct Grid {
     int64_t tiles, streams;
 };
 
-constexpr int kCus = 256;
-
 Grid grid_of(const AttnArgs &a) {
     if (a.dtype != SGMV_BF16) return {0, most_groups(a, a.num_requests, kStreamRows) * a.kv_heads + kStreamTarget};
     // A batch whose requests are all short is the streaming kernel's alone.
@@ -1129,6 +1127,8 @@ bool is_streamed(const AttnArgs &a) {
     const int64_t rows = (int64_t)a.max_q_len * a.group, groups = (int64_t)a.num_requests * a.kv_heads;
     return a.dtype != SGMV_BF16 || rows <= (groups <= 2 * kTileTarget ? 2 * kStreamRows : kStreamRows);
 }
+
+constexpr int kCus = 256;
 
 // Adds up the splits of the launch before, if it can have any.
 template <typename T, typename Kind>

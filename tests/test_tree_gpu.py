@@ -349,6 +349,43 @@ def test_tree_accept(dev, B, lo, hi, page, agree, refused):
                tail=B % 4)
 
 
+@pytest.mark.parametrize("sizes,tail", [
+    ([64] * 64, 0), ([64] * 64, 1), ([64] * 63 + [0], 64), ([1] * 64, 3), ([1] * 65, 0), ([0] * 31 + [4096], 0), ([17] * 16 + [0] * 3, 2)],
+    ids=["4096", "4097", "tail", "64of1", "65of1", "one", "odd"])
+def test_accept_of_full_and_empty_workgroups(dev, sizes, tail):
+    rng = np.random.default_rng(len(sizes) + tail)
+    refused = (2, 5) if len(sizes) > 16 else ()
+    run_accept(dev, accept_case(rng, sizes, [int(x) for x in rng.integers(0, 90, len(sizes))], 16, 0.9, refused=refused), tail=tail)
+
+
+def test_accept_of_large_steps(dev):
+    """Chains longer than what is looked at, and many requests' pages that wrap round the ring's end."""
+    rng = np.random.default_rng(3)
+    c = accept_case(rng, [1030, 3100], [5, 0], 16, 0.0)
+    c["parents"] = [np.arange(-1, 1029), np.arange(-1, 3099)]
+    c["token"], c["target"] = np.arange(4130), np.arange(1, 4131)
+    assert run_accept(dev, c)["accepted"].tolist() == [1024, 1024]
+    c = accept_case(rng, [90] * 70, [int(x) for x in rng.integers(0, 50, 70)], 16, 1.0, vocabulary=2, free=0)
+    c["pool"][0] = len(c["ring"]) - 2
+    run_accept(dev, c)
+
+
+def test_accept_of_large_steps_with_bad_device_values(dev):
+    rng = np.random.default_rng(5)
+    c = accept_case(rng, [2100, 2100], [10, 20], 16, 0.7)
+    T, big = 4200, 2 ** 30
+    guard = torch.full((9, T), 7, dtype=torch.int32, device=dev)
+    for parent, q_start, kv, pool in (
+            (rng.integers(-big, big, T), [0, 2100, T], [big, -big], [-5, big, 0, 0]),
+            (np.arange(T), [-9, big, 3], [0, 5], [big, -1, 0, 0])):
+        ring = torch.full((3, len(c["ring"])), 7, dtype=torch.int32, device=dev)
+        sg.sgmv_tree_accept(ints(parent, dev), ints(c["token"], dev), ints(c["token"], dev), ints(c["slot"], dev), ints(q_start, dev),
+                            ints(kv, dev), 16, ints(c["block_table"], dev), ring[1], ints(pool, dev), guard[1, :4], guard[3],
+                            guard[5, :2], guard[5, 2:4], guard[5, 4:6])
+        assert bool((ring[[0, 2]] == 7).all())
+        assert bool((guard[[0, 2, 4, 6, 7, 8]] == 7).all()) and bool((guard[5, 6:] == 7).all()) and bool((guard[1, 4:] == 7).all())
+
+
 def test_accept_ties_chain_and_ring(dev):
     rng = np.random.default_rng(2)
     c = accept_case(rng, [90, 8], [10, 0], 16, 1.0, vocabulary=2)      # many children hold the same token: the first
