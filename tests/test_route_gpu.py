@@ -69,6 +69,14 @@ def test_sort(dev, T, k, P, absent):
             assert np.array_equal(g.cpu().numpy(), w), name
 
 
+@pytest.mark.parametrize("T,k,P", [(1 << 23, 2, 4096), ((1 << 24) - 5, 1, 130)])
+def test_sort_of_the_most_choices(dev, T, k, P):
+    choice = np.random.default_rng(P).integers(-1, P, (T, k), dtype=np.int32)
+    got, want = run_sort(dev, choice, P)
+    for g, w, name in zip(got, want, ("seg_start", "seg_adapter", "order", "place")):
+        assert np.array_equal(g.cpu().numpy(), w), name
+
+
 @pytest.mark.parametrize("T", [50, 5000])
 def test_sort_of_one_choice_is_the_host_grouping(dev, T):
     """With one adapter per token: what sgmv_build_segments gives, and the gathered calls take order as rows."""

@@ -194,14 +194,14 @@ def test_long_context_is_split(dev, dtype, n):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("n", [9, 70])
-def test_values_that_are_not_finite_reach_the_rows_that_see_them(dev, dtype, n):
+@pytest.mark.parametrize("n,ctx", [(9, 50), (70, 50), (9, 9000), (70, 9000)], ids=["9", "70", "9split", "70split"])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(dev, dtype, n, ctx):
     """NaN and infinities in drafted tokens' keys and values, and in a cached value: a row is what the formula says, and
     a row that does not see them is bitwise what it is without them."""
     rng = np.random.default_rng(n)
-    x, h = make(dev, rng, [n], [50], 4, 2, 64, dtype, 16)
+    x, h = make(dev, rng, [n], [ctx], 4, 2, 64, dtype, 16)
     clean, clean_lse = attend(x, 0.125, n)
-    cell = lambda m: (int(h["block_table"][0, (50 + m) // 16]), (50 + m) % 16)  # noqa: E731
+    cell = lambda m: (int(h["block_table"][0, (ctx + m) // 16]), (ctx + m) % 16)  # noqa: E731
     hit = [2, n - 1]
     for m, (k, v) in zip(hit, [(None, float("inf")), (float("nan"), 3.0)]):
         p, o = cell(m)
@@ -217,6 +217,29 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(dev, dtype, n):
             assert bool(out[i].isnan().all()) and bool(lse[i].isnan().all()), i
         else:
             assert bool((out[i] == float("inf")).all()) and torch.equal(lse[i], clean_lse[i]), i
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n,ctx", [(9, 300), (70, 300), (9, 9000), (70, 9000)])
+def test_cached_values_that_are_not_finite(dev, dtype, n, ctx):
+    """A cached infinity that every row sees, in a part of its own where the keys are split, and one that a window hides
+    from every row: the first is every row's result in its column, the second nobody's."""
+    rng = np.random.default_rng(ctx + n)
+    x, h = make(dev, rng, [n], [ctx], 4, 2, 64, dtype, 16)
+    cell = lambda j: (int(h["block_table"][0, j // 16]), j % 16)  # noqa: E731
+    for window in (0, 200):
+        clean, clean_lse = attend(x, 0.125, n, window)
+        V = x["V"].clone()
+        p, o = cell(ctx - 30)
+        V[p, 0, o, 5], V[p, 1, o, 60] = float("-inf"), float("nan")
+        hidden = cell(40)
+        if window:
+            V[hidden[0], :, hidden[1]] = float("nan")
+        out, lse = attend(dict(x, V=V), 0.125, n, window)
+        assert torch.equal(lse, clean_lse)
+        assert bool((out[:, :2, 5] == float("-inf")).all()) and bool(out[:, 2:, 60].isnan().all())
+        out[:, :2, 5], out[:, 2:, 60] = clean[:, :2, 5], clean[:, 2:, 60]
+        assert torch.equal(out, clean)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
