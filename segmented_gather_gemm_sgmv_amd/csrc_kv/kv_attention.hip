@@ -1135,7 +1135,7 @@ template <typename T, typename Kind>
 void launch_join(const AttnArgs &a, const float *slots, hipStream_t st) {
     if (most_tiles(a, Kind::kKeys) < Kind::kMinTiles) return;
     const auto kernel = a.head_dim <= 64 ? join_kernel<T, 64, Kind> : join_kernel<T, 128, Kind>;
-    hipLaunchKernelGGL(kernel, dim3(3 * kCus), dim3(kThreads), 0, st, a, slots);  // a group in parts has 683 at most
+    hipLaunchKernelGGL(kernel, dim3(3 * kCus), dim3(join_waves<Kind> * kWave), 0, st, a, slots);  // a group in parts has 683 at most
 }
 
 }  // namespace

@@ -351,6 +351,13 @@ __device__ __forceinline__ void tree_tile_item(const AttnArgs &a, const Item &it
 // 67 us in all, 9.9 of it here (31 MB), and 104 with the last workgroup's. A
 // launch without splits costs 4.8 us, where the table of pages allows any.
 // ----------------------------------------------------------------------------
+// Waves of its workgroups. Of 128 rows a part has 4 or more, and with 8 waves fewer come one after another: 4 requests of
+// 25 tokens behind 2000, 64 heads on 8, 43.6 -> 37.8 us in all, 32 of 16 behind up to 4000 128 -> 119; 16 waves 36.5 and 119,
+// but start later: 72.7 for 70.3 with the one request above. Of 16 rows 4 waves have enough: one token behind 31000 32.4 us,
+// with 8 waves 33.0.
+template <typename Kind>
+constexpr int join_waves = Kind::kRows > kStreamRows ? 8 : 4;
+
 template <typename T, int D, typename Kind>
 __device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, const float *slots) {
     constexpr int kRows = Kind::kRows, kSlot = kRows * D + 2 * kRows, kPer = D / 64, kRegs = (Kind::kMaxSplits + 63) / 64, kDeep = 16;
@@ -360,7 +367,7 @@ __device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, con
     const int tid = this_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row0 = it.row_tile * kRows, live = min(kRows, it.n * a.group - row0);
     const float *part = slots + (int64_t)it.first_slot * kSlot;
-    for (int row = live * it.split / splits + wave; row < live * (it.split + 1) / splits; row += kWaves) {
+    for (int row = live * it.split / splits + wave; row < live * (it.split + 1) / splits; row += join_waves<Kind>) {
         float f[kRegs], l[kRegs], top = kNone, weight = 0.f;
 #pragma unroll
         for (int i = 0; i < kRegs; ++i) {
@@ -417,7 +424,7 @@ __device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, con
 }
 
 template <typename T, int D, typename Kind>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a, const float *slots) {
+__global__ __launch_bounds__(join_waves<Kind> * kWave) void join_kernel(AttnArgs a, const float *slots) {
     each_split<Kind>(a, blockIdx.x, gridDim.x, [&](const Item &it) { join_item<T, D, Kind>(a, it, slots); });
 }
 
