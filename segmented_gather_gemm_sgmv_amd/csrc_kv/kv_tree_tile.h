@@ -346,10 +346,10 @@ __device__ __forceinline__ void tree_tile_item(const AttnArgs &a, const Item &it
 // Adding up the splits of a tree's groups, in a launch of its own: a group of
 // 128 rows in 32 splits is 2 MB, which the last of its workgroups alone would
 // read at the latency of 16 loads a lane. Here split k's workgroup adds the k-th
-// part of the group's rows, a wave a row; the workgroups look for their groups
-// as the attention's do. One request of 25 tokens behind 31000, 64 heads on 8:
-// 67 us in all, 9.9 of it here (31 MB), and 104 with the last workgroup's. A
-// launch without splits costs 4.8 us, where the table of pages allows any.
+// part of the group's rows; the workgroups look for their groups as the
+// attention's do. One request of 25 tokens behind 31000, 64 heads on 8: 66 us
+// in all, 8.2 of it here (31 MB), and 104 with the last workgroup's. A launch
+// without splits costs 4.6 us, where the table of pages allows any.
 // ----------------------------------------------------------------------------
 // Waves of its workgroups. Of 128 rows a part has 4 or more, and with 8 waves fewer come one after another: 4 requests of
 // 25 tokens behind 2000, 64 heads on 8, 43.6 -> 37.8 us in all, 32 of 16 behind up to 4000 128 -> 119; 16 waves 36.5 and 119,
@@ -358,69 +358,107 @@ __device__ __forceinline__ void tree_tile_item(const AttnArgs &a, const Item &it
 template <typename Kind>
 constexpr int join_waves = Kind::kRows > kStreamRows ? 8 : 4;
 
-template <typename T, int D, typename Kind>
-__device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, const float *slots) {
-    constexpr int kRows = Kind::kRows, kSlot = kRows * D + 2 * kRows, kPer = D / 64, kRegs = (Kind::kMaxSplits + 63) / 64, kDeep = 16;
-    const TileRun run = tile_run<Kind::kKeys>(it.p0 - 1, it.p0 + it.n - 1, a.window, a.sinks);
-    const int splits = (run.count + it.size - 1) / it.size;
-    if (it.split >= splits) return;
+// Rows [begin, end) of a group in `splits` parts; a wave takes kR of them at once, 16 loads deep, so that few parts leave
+// no load without use: 4 requests of 25 tokens behind 2000 12.4 -> 8.0 us here, 32 of 16 behind up to 4000 27.0 -> 15.5.
+// What it reads first waits for nothing.
+template <typename T, int D, typename Kind, int kR>
+__device__ __forceinline__ void join_rows(const AttnArgs &a, const Item &it, const float *part, int splits, int begin, int end) {
+    constexpr int kRows = Kind::kRows, kSlot = kRows * D + 2 * kRows, kPer = D / 64, kDeep = 16 / kR, kStep = join_waves<Kind>;
+    constexpr int kRegs = kR > 1 ? 1 : (Kind::kMaxSplits + 63) / 64;
     const int tid = this_thread(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int row0 = it.row_tile * kRows, live = min(kRows, it.n * a.group - row0);
-    const float *part = slots + (int64_t)it.first_slot * kSlot;
-    for (int row = live * it.split / splits + wave; row < live * (it.split + 1) / splits; row += join_waves<Kind>) {
-        float f[kRegs], l[kRegs], top = kNone, weight = 0.f;
+    for (int first = begin + wave; first < end; first += kStep * kR) {
+        int row[kR];
+        float x[kR][kDeep][kPer], f[kR][kRegs], l[kR][kRegs], top[kR], weight[kR], sum[kR][kPer];
+        const auto load = [&](int k0) {
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            const int k = 64 * i + lane;
-            f[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + row] : kNone;
-            l[i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + kRows + row] : 0.f;
-            top = fmaxf(top, f[i]);
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            f[i] = exp2_fast(f[i] - ref_of(top));
-            weight += f[i] * l[i];
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) weight += __shfl_xor(weight, o);
-        float sum[kPer];
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) sum[c] = 0.f;
-        const float *from = part + (int64_t)row * D + kPer * lane;
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            for (int k0 = 64 * i; k0 < min(splits, 64 * i + 64); k0 += kDeep) {
-                float x[kDeep][kPer];
+            for (int r = 0; r < kR; ++r)
 #pragma unroll
                 for (int j = 0; j < kDeep; ++j)
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c) x[j][c] = from[(int64_t)min(k0 + j, splits - 1) * kSlot + c];
+                    for (int c = 0; c < kPer; ++c)
+                        x[r][j][c] = part[(int64_t)min(k0 + j, splits - 1) * kSlot + (int64_t)row[r] * D + kPer * lane + c];
+        };
 #pragma unroll
-                for (int j = 0; j < kDeep; ++j) {
-                    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[i]), (k0 + j) & 63));
+        for (int r = 0; r < kR; ++r) {
+            row[r] = min(first + r * kStep, end - 1);
 #pragma unroll
-                    for (int c = 0; c < kPer; ++c)  // a value that is not finite is that value under any weight
-                        sum[c] += k0 + j >= splits ? 0.f : is_finite(x[j][c]) ? x[j][c] * w : x[j][c];
+            for (int i = 0; i < kRegs; ++i) {
+                const int k = 64 * i + lane;
+                f[r][i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + row[r]] : kNone;
+                l[r][i] = k < splits ? part[(int64_t)k * kSlot + kRows * D + kRows + row[r]] : 0.f;
+            }
+        }
+        load(0);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            top[r] = kNone;
+            weight[r] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) top[r] = fmaxf(top[r], f[r][i]);
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) top[r] = fmaxf(top[r], __shfl_xor(top[r], o));
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) {
+                f[r][i] = exp2_fast(f[r][i] - ref_of(top[r]));
+                weight[r] += f[r][i] * l[r][i];
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) weight[r] += __shfl_xor(weight[r], o);
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) sum[r][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+            for (int k0 = 64 * i; k0 < min(splits, 64 * i + 64); k0 += kDeep) {
+                if (k0 > 0) load(k0);
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int j = 0; j < kDeep; ++j) {
+                        const float w = __builtin_bit_cast(
+                            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[r][i]), (k0 + j) & 63));
+#pragma unroll
+                        for (int c = 0; c < kPer; ++c)  // a value that is not finite is that value under any weight
+                            sum[r][c] += k0 + j >= splits ? 0.f : is_finite(x[r][j][c]) ? x[r][j][c] * w : x[r][j][c];
+                    }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if (first + r * kStep >= end) break;
+            const int at = it.row_tile * kRows + row[r], head = it.head * a.group + at % a.group, col = kPer * lane;
+            const int64_t q_row = it.q0 + at / a.group;
+            const float inv = weight[r] > 0.f || weight[r] != weight[r] ? 1.f / weight[r] : 0.f;
+            if (col < a.head_dim) {
+                T *dst = static_cast<T *>(a.out) + q_row * a.out_stride + (int64_t)head * a.head_dim + col;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) {
+                    if constexpr (sizeof(T) == 2)
+                        dst[c].bits = __builtin_bit_cast(uint16_t, (__bf16)(sum[r][c] * inv));
+                    else
+                        dst[c] = sum[r][c] * inv;
                 }
             }
+            if (a.lse && lane == 0) a.lse[q_row * a.q_heads + head] = lse_of(top[r], weight[r]);
         }
-        const int at = row0 + row, head = it.head * a.group + at % a.group, col = kPer * lane;
-        const int64_t q_row = it.q0 + at / a.group;
-        const float inv = weight > 0.f || weight != weight ? 1.f / weight : 0.f;
-        if (col < a.head_dim) {
-            T *dst = static_cast<T *>(a.out) + q_row * a.out_stride + (int64_t)head * a.head_dim + col;
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-                if constexpr (sizeof(T) == 2)
-                    dst[c].bits = __builtin_bit_cast(uint16_t, (__bf16)(sum[c] * inv));
-                else
-                    dst[c] = sum[c] * inv;
-            }
-        }
-        if (a.lse && lane == 0) a.lse[q_row * a.q_heads + head] = lse_of(top, weight);
     }
+}
+
+template <typename T, int D, typename Kind>
+__device__ __forceinline__ void join_item(const AttnArgs &a, const Item &it, const float *slots) {
+    constexpr int kRows = Kind::kRows, kSlot = kRows * D + 2 * kRows;
+    const TileRun run = tile_run<Kind::kKeys>(it.p0 - 1, it.p0 + it.n - 1, a.window, a.sinks);
+    const int splits = (run.count + it.size - 1) / it.size;
+    if (it.split >= splits) return;
+    const int live = min(kRows, it.n * a.group - it.row_tile * kRows);
+    const float *part = slots + (int64_t)it.first_slot * kSlot;
+    const int begin = live * it.split / splits, end = live * (it.split + 1) / splits;
+    if (splits <= 4)
+        join_rows<T, D, Kind, 4>(a, it, part, splits, begin, end);
+    else if (splits <= 8)
+        join_rows<T, D, Kind, 2>(a, it, part, splits, begin, end);
+    else
+        join_rows<T, D, Kind, 1>(a, it, part, splits, begin, end);
 }
 
 template <typename T, int D, typename Kind>
