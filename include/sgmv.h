@@ -618,6 +618,12 @@ int sgmv_tree_attention(void *out, int64_t out_stride, float *lse, const void *q
  * have no slot), nothing is accepted, and its length stays. At most the first
  * 32 * SGMV_MAX_TREE_WORDS tokens of a request are looked at.
  *
+ * Every request of the step is verified, one that adds a run of tokens (a
+ * prompt, or a chunk of one) too. To keep a run whole give it as a chain,
+ * parent[i] = i - 1, with target[i] = token[i + 1] for all of its tokens but
+ * the last; it is then no longer than a tree, 32 * mask_words tokens, and a
+ * longer prompt goes in several steps or in one without trees.
+ *
  * Pages that hold none of the kept_len[b] tokens go back behind the free ones
  * of the ring, requests in order. block_table is left as it is (sgmv_kv_commit
  * goes by slot, and entries past a request's length have no meaning to the

@@ -899,7 +899,10 @@ class PagedKVCache:
                accepted: torch.Tensor, next_token: torch.Tensor, stream=None) -> None:
         """Keeps, of the step's trees, what the model agrees with: target[T] is its own token after each of the step's
         tokens. Writes path [T], accepted and next_token [max_requests] (sgmv_tree_accept); kv_len and the pool are those
-        without the other tokens from here on. Once per step, after its last ``attend``."""
+        without the other tokens from here on. Once per step, after its last ``attend``.
+
+        All requests are verified: a prompt in a drafted step is a chain (parent[i] = i - 1) of at most 32 * words tokens,
+        and is kept whole where target[i] is its own token i + 1 (the model's at its last one only)."""
         self._use_slots(stream)
         sgmv_tree_accept(parent, token, target, self.slot, self.q_start, self._len[0], self.page_size, self.block_table,
                          self.free_pages, self._pool[0], self._pool[1], path, accepted, next_token, self._len[1], stream)
