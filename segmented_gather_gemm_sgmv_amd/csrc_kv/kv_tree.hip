@@ -190,9 +190,10 @@ __global__ __launch_bounds__(kThreads) void give_back_kernel(AcceptArgs a) {
 // in order: since path grows, path[d] >= d, a row is read before it is
 // overwritten, and lanes have no bytes in common, so nothing else is waited
 // for. Up to kDeep rows are in flight.
-// Measured (kernel alone): 64 requests, one layer of 32 heads of 128, 4.4 us;
-// 256 requests, eight layers of 8 heads, some 49 MB read and written, 12.0 us
-// (4.1 TB/s; a copy reaches 4.7).
+// Measured (kernel alone): 64 requests, one layer of 32 heads of 128, 4.4 us
+// for some 143 rows that move (4.7 MB); 256 requests, eight layers of 8 heads,
+// 570 to 630 rows, 37 to 41 MB read and written, 12.0 us (3.2 TB/s; a copy
+// reaches 4.7).
 // ----------------------------------------------------------------------------
 constexpr int kDeep = 4;
 
