@@ -4,11 +4,12 @@
 //
 // The tile kernel is the causal one's (128 rows on four waves, tiles of 64 keys
 // in two buffers) with three differences. Its rows see the cached keys alike,
-// so that a tile is bounded by the request, not by the row, and only the last
-// tiles look at masks. A row tile of up to 64 rows, which a request with heads
-// of its own has, would leave two waves idle: they take the other half of each
-// tile's keys, and the halves' results meet in LDS. And a split group's parts
-// are added up by another launch.
+// so that a tile is bounded by the request, not by the row, and only tiles that
+// reach past the cached keys (for n new tokens (n + 62) / 64 + 1 at most) or lie
+// on a window's edge look at masks. A row tile of up to 64 rows, which a request
+// with heads of its own has, would leave two waves idle: they take the other half
+// of each tile's keys, and the halves' results meet in LDS. And a split group's
+// parts are added up by another launch.
 //
 // What bounds it: with many rows the matrix cores and the softmax beside them,
 // at the clock that the power limit leaves (128 trees of 64 tokens behind 127

@@ -4,15 +4,18 @@
 // What bounds them: HBM. A lane takes 16 bytes of a token's row: spread reads
 // them once and writes them to each of the token's rows in segment order;
 // combine reads them from each of these and writes their sum once; grad reads
-// dY's and Ys's once and keeps the products' sums. Going by tokens rather than
-// by rows in segment order, every element is read once and written once, and
-// a sum has one lane and one order.
+// dY's and Ys's and keeps the products' sums. Going by tokens rather than by
+// rows in segment order, every element is read once and written once, and a sum
+// has one lane and one order; only grad reads a token's dY again for every four
+// choices after the first four.
 //
 // Measured (kernels alone, bf16): 4583 tokens to 17415 rows of 8192, 360 MB, 69
 // us (5.2 TB/s); back, weighted, onto a base, 435 MB, 66 us (6.5); the gradient
 // of 4583 tokens over 8700 rows of 4096, 180 MB, 32 us (5.6); 64 tokens and 115
 // rows of 4096 2.9 us each way. The halves of a workgroup, 128 threads, made
-// no difference.
+// no difference. The gradient of 4583 tokens a call, of eight choices over rows
+// of 4096 115 us; of two over rows of 512 10.3 us, and of 64, where 8 lanes of a
+// token's 256 have something to do, 8.9.
 #include "route_launch.h"
 #include "sgmv.h"
 #include "sgmv_common.h"
