@@ -1123,6 +1123,9 @@ namespace {
 // and splits finer. Up to 32 rows it is as good or better where the GPU has no more groups than it runs at once, 64 heads on
 // 8: 4 requests of 4 tokens over 2000 keys 18 us against 24, 64 over 127 to 4095 122 against 125; with many the second
 // pass over the keys costs more: 64 requests of 32 tokens over up to 2047, 32 heads of their own, 249 against 217.
+// It is decided for the batch, by the most tokens that a request can have, so a few trees put single tokens beside them
+// into tiles too: 256 requests of one token and 4 of 64, over 127 to 4095, 64 heads on 8 450 us, and 429 as two calls
+// (372 and 54 alone); 32 heads of their own 1618 and 1437.
 bool is_streamed(const AttnArgs &a) {
     const int64_t rows = (int64_t)a.max_q_len * a.group, groups = (int64_t)a.num_requests * a.kv_heads;
     return a.dtype != SGMV_BF16 || rows <= (groups <= 2 * kTileTarget ? 2 * kStreamRows : kStreamRows);
