@@ -685,8 +685,11 @@ int sgmv_kv_commit(void *K_cache, void *V_cache, int32_t num_layers, int64_t lay
  * Xs, Ys, dYs, dXs   `rows` rows of d elements, in segment order.
  * X, Y, base, dY, dX   T rows of d elements, in token order.
  * Row strides are in elements; rows start 16-byte aligned. d is a positive
- * multiple of 8, choices 1 .. SGMV_MAX_CHOICES. Sums are fp32, in the order of
- * the choices, and rounded once. Streams, ownership, errors and what is
+ * multiple of 8, choices 1 .. SGMV_MAX_CHOICES, T * choices at most 2^24. A
+ * launch has fewer than 2^24 workgroups (one per token in the gradient, and one
+ * per token and 4 KB of its row in the others where a row has more than 512
+ * bytes): a call that needs more is refused with SGMV_ERR_SHAPE. Sums are fp32,
+ * in the order of the choices, and rounded once. Streams, ownership, errors and what is
  * promised for any device-resident values are as above.
  */
 #define SGMV_MAX_CHOICES 64

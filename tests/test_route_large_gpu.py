@@ -1,6 +1,7 @@
 """Row calls that move more than 256 MiB, whose results are written as streams,
 and calls just below that: against 64 bits, and against the same rows taken in
-smaller calls, bit for bit. The last-level cache holds 256 MiB."""
+smaller calls, bit for bit. The last-level cache holds 256 MiB. And as many
+tokens as one launch has workgroups for."""
 import pytest
 import torch
 
@@ -129,3 +130,21 @@ def test_combine_grad(dev, dtype, above, k, d, which):
             if which != "rows":  # a sum of d products, in any order
                 terms = torch.where(on[:, None], g * Ys[at].double(), 0.0)
                 assert bool(((dweight[p, j].double() - terms.sum(1)).abs() <= (d + 2) * U32 * terms.abs().sum(1)).all())
+
+
+def test_the_most_tokens(dev):
+    """The gradient takes a workgroup per token, of which one launch has fewer than 2^24."""
+    T, d = (1 << 24) - 1, 8
+    gen = torch.Generator(dev).manual_seed(2)
+    place = torch.randperm(T, generator=gen, device=dev).int().view(T, 1)
+    dY, Ys = (torch.randn(T, d, generator=gen, device=dev) for _ in range(2))
+    weight = torch.randn(T, 1, generator=gen, device=dev)
+    dYs, dweight = torch.zeros_like(Ys), torch.zeros_like(weight)
+    sg.sgmv_combine_rows_grad(dYs, dweight, dY, Ys, place, weight)
+    at = place[:, 0].long()
+    assert torch.equal(dYs[at], weight * dY)
+    terms = dY.double() * Ys[at].double()
+    assert bool(((dweight[:, 0].double() - terms.sum(1)).abs() <= (d + 2) * U32 * terms.abs().sum(1)).all())
+    with pytest.raises(sg.SGMVError):
+        sg.sgmv_combine_rows_grad(None, torch.zeros(T + 1, 1, device=dev), torch.zeros(T + 1, d, device=dev), Ys,
+                                  torch.zeros(T + 1, 1, dtype=torch.int32, device=dev))
