@@ -221,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs a, int run, in
         done.y += total.y;
     }
     if (blockIdx.x == 0) {
-        for (int s = done.y + tid; s <= a.num_segments; s += kThreads) {
+        for (int64_t s = done.y + tid; s <= a.num_segments; s += kThreads) {  // up to 2^31 - 1 segments: past it an int would not end
             a.seg_start[s] = done.x;
             if (s < a.num_segments) a.seg_adapter[s] = 0;
         }

@@ -148,3 +148,19 @@ def test_the_most_tokens(dev):
     with pytest.raises(sg.SGMVError):
         sg.sgmv_combine_rows_grad(None, torch.zeros(T + 1, 1, device=dev), torch.zeros(T + 1, d, device=dev), Ys,
                                   torch.zeros(T + 1, 1, dtype=torch.int32, device=dev))
+
+
+def test_the_most_segments(dev):
+    """2^31 - 1 segments, all but three of them empty."""
+    S = 2 ** 31 - 1
+    if torch.cuda.mem_get_info(dev)[0] < 24 << 30:
+        pytest.skip("needs 24 GB of GPU memory")
+    choice = torch.tensor([[3], [1], [3], [-1], [0]], dtype=torch.int32, device=dev)
+    start, adapter = (torch.full((n,), 77, dtype=torch.int32, device=dev) for n in (S + 1, S))
+    order, place = torch.empty(5, dtype=torch.int32, device=dev), torch.empty_like(choice)
+    sg.sgmv_sort_tokens(choice, 4, start, adapter, order, place)
+    assert order.tolist() == [4, 1, 0, 2, -1] and place.view(-1).tolist() == [2, 1, 3, -1, 0]
+    assert start[:3].tolist() == [0, 1, 2] and adapter[:3].tolist() == [0, 1, 3]
+    step = 1 << 28
+    assert all(bool((start[max(i, 3):i + step] == 4).all()) for i in range(0, S + 1, step))
+    assert all(bool((adapter[max(i, 3):i + step] == 0).all()) for i in range(0, S, step))
