@@ -222,10 +222,9 @@ inline size_t layer_workspace_total(const LayerProjIn *p, int num_projections, i
 // Workgroups of the largest launch one projection of a call makes (the
 // fused launch: vector shrink, MFMA shrink, vector expand and MFMA expand
 // items, each region padded to a multiple of 8), counted in 64 bits. The
-// kernels number their workgroups with int, and one dispatch holds fewer than
-// 2^32 work-items (the packet's grid size is 32 bits), so fewer than 2^24
-// workgroups: calls beyond kMaxWorkgroups are refused.
-constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;
+// kernels number their workgroups with int, and one dispatch holds at most
+// 2^32 work-items, 2^24 workgroups: calls beyond kMaxWorkgroups are refused.
+constexpr int64_t kMaxWorkgroups = (int64_t)1 << 24;
 inline int64_t launch_workgroups(int M, int num_segments, int d_in, int d_out, int r, int dtype) {
     auto pad8 = [](int64_t n) { return (n + 7) / 8 * 8; };
     const ShrinkPlan P = shrink_plan(M, d_in, r, dtype);

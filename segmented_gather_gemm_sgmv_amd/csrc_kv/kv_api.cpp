@@ -15,6 +15,10 @@ namespace {
 
 int hip_status(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_ERR_HIP; }
 
+// One dispatch holds fewer than 2^32 work-items (its packet has 32 bits for them): 2^24 workgroups of 256 threads are one
+// too many.
+bool too_many(int64_t workgroups) { return workgroups >= sgmv::kMaxWorkgroups; }
+
 // The exponent of a valid page size, or -1.
 int page_shift(int32_t page_size) {
     for (int s = 4; s <= 8; ++s)
@@ -80,7 +84,7 @@ int attention(void *out, int64_t out_stride, float *lse, const void *q, int64_t 
                            q_start,   kv_len,       num_requests, T,       max_q_len < T ? max_q_len : T,
                            scale,     window < far ? window : far, sinks < far ? sinks : far, dtype, workspace,
                            mask,      mask_words};
-    if ((tree ? sgmv::tree_attention_workgroups(a) : sgmv::attention_workgroups(a)) > sgmv::kMaxWorkgroups)
+    if (too_many(tree ? sgmv::tree_attention_workgroups(a) : sgmv::attention_workgroups(a)))
         return SGMV_ERR_SHAPE;
     const hipStream_t on = static_cast<hipStream_t>(stream);
     return hip_status(tree ? sgmv::launch_tree_attention(a, on) : sgmv::launch_paged_attention(a, on));
@@ -169,7 +173,7 @@ int sgmv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q
                            k_stride,  v,            v_stride,   K_cache,   V_cache,   num_pages,
                            kv_heads,  kv_heads > 0 ? page_shift(page_size) : 4, head_dim, position, slot, T,
                            table,     max_position, rot_dim,    interleaved, dtype};
-    if (sgmv::rope_append_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
+    if (too_many(sgmv::rope_append_workgroups(a))) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_rope_append(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -251,7 +255,7 @@ int sgmv_kv_commit(void *K_cache, void *V_cache, int32_t num_layers, int64_t lay
     const sgmv::CommitArgs a{K_cache,  V_cache, num_layers, num_layers > 1 ? layer_stride : 0, num_pages, kv_heads,
                              page_shift(page_size), head_dim, dtype, slot, q_start, path, num_requests, T};
     const int64_t groups = sgmv::kv_commit_workgroups(a);
-    if (groups > sgmv::kMaxWorkgroups || groups / num_requests > 65535) return SGMV_ERR_SHAPE;
+    if (too_many(groups) || groups / num_requests > 65535) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_kv_commit(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -13,6 +13,10 @@ namespace {
 
 int hip_status(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_ERR_HIP; }
 
+// One dispatch holds fewer than 2^32 work-items (its packet has 32 bits for them): 2^24 workgroups of 256 threads are one
+// too many.
+bool too_many(int64_t workgroups) { return workgroups >= sgmv::kMaxWorkgroups; }
+
 constexpr int64_t kMostChoices = 1 << 24;
 
 // Sizes that the calls share.
@@ -65,7 +69,7 @@ int sgmv_spread_rows(void *Xs, int64_t Xs_stride, int32_t rows, const void *X, i
     if (st == SGMV_OK) st = check_rows(X, X_stride, T, d, dtype);
     if (st != SGMV_OK) return st;
     const sgmv::RowsArgs a{Xs, Xs_stride, X, X_stride, nullptr, 0, rows, place, nullptr, nullptr, T, choices, d, dtype};
-    if (sgmv::rows_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
+    if (too_many(sgmv::rows_workgroups(a))) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_spread_rows(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -81,7 +85,7 @@ int sgmv_combine_rows(void *Y, int64_t Y_stride, const void *base, int64_t base_
     if (st == SGMV_OK && rows > 0) st = check_rows(Ys, Ys_stride, rows, d, dtype);
     if (st != SGMV_OK) return st;
     const sgmv::RowsArgs a{Y, Y_stride, base, base_stride, Ys, Ys_stride, rows, place, weight, nullptr, T, choices, d, dtype};
-    if (sgmv::rows_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
+    if (too_many(sgmv::rows_workgroups(a))) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_combine_rows(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -98,7 +102,7 @@ int sgmv_combine_rows_grad(void *dYs, int64_t dYs_stride, float *dweight, const 
     if (st == SGMV_OK && dweight && rows > 0) st = check_rows(Ys, Ys_stride, rows, d, dtype);
     if (st != SGMV_OK) return st;
     const sgmv::RowsArgs a{dYs, dYs_stride, dY, dY_stride, Ys, Ys_stride, rows, place, weight, dweight, T, choices, d, dtype};
-    if (sgmv::rows_workgroups(a) > sgmv::kMaxWorkgroups) return SGMV_ERR_SHAPE;
+    if (too_many(sgmv::rows_workgroups(a))) return SGMV_ERR_SHAPE;
     return hip_status(sgmv::launch_combine_rows_grad(a, static_cast<hipStream_t>(stream)));
 }
 
